@@ -1,0 +1,166 @@
+/*
+ * kda_layer.h -- C ABI of the operators a KDA linear-attention layer runs
+ * around its short conv (kda_conv.h), GB300 (sm_103a):
+ *   - the gated delta rule over a packed varlen batch (prefill) and for one
+ *     token per sequence (decode), on a paged FP32 state;
+ *   - the per-head RMS norm with the layer's output gate that follows it;
+ *   - the norms before and after a block, fused with its gate and the scaled
+ *     residual add.
+ * Conventions are those of kda_conv.h: device pointers owned by the caller,
+ * calls asynchronous on `stream`, nothing allocated, nothing synchronised,
+ * kernels and grids that depend only on the scalar arguments (CUDA-graph
+ * safe), every kernel launched as a programmatic dependent of the one before
+ * it. Argument errors return before any CUDA call.
+ */
+#ifndef KDA_LAYER_H_
+#define KDA_LAYER_H_
+
+#include "kda_conv.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* How kda_delta_t::gate is read. */
+typedef enum {
+    KDA_GATE_LOG = 0,     /* the log decay itself (<= 0) */
+    KDA_GATE_SOFTPLUS = 1 /* raw: g = -exp(a_log[h]) * softplus(raw + dt_bias[h][k]) */
+} kda_gate_t;
+
+/* How kda_delta_t::beta is read. */
+typedef enum { KDA_BETA_PLAIN = 0, KDA_BETA_SIGMOID = 1 } kda_beta_t;
+
+/* Gate of the norm entry points. */
+typedef enum { KDA_NORM_GATE_NONE = 0, KDA_NORM_GATE_SIGMOID = 1, KDA_NORM_GATE_SILU = 2 } kda_norm_gate_t;
+
+/*
+ * The gated delta rule. For each head, with S the D x D state S[v][k] (D =
+ * head_dim), a sequence's tokens t are taken in order:
+ *     S   = S * diag(exp(g_t))                 g_t[k] per channel, or one g_t per head
+ *     u   = beta_t * (v_t - S k_t)
+ *     S   = S + u k_t^T
+ *     o_t = scale * S q_t
+ * All sums, decays and the state are FP32 (the chunked path carries its tensor
+ * core operands as pairs of halves, 22 bits, so that the state keeps FP32's
+ * accuracy). out is rounded to nearest even.
+ *
+ *   q, k, v, out  (tokens, heads, D) of x_dtype, channels contiguous, with token
+ *                 and head strides in elements. The planes of the packed conv's
+ *                 output are such tensors (token stride part_dim, head stride D).
+ *                 16-byte aligned, strides multiples of 16 bytes. out must not
+ *                 overlap the inputs.
+ *   gate          KDA_GATE_LOG or KDA_GATE_SOFTPLUS values of gate_dtype. With
+ *                 gate_per_channel 1: (tokens, heads, D), channels contiguous,
+ *                 aligned as q. With 0: (tokens, heads), one decay per head, any
+ *                 strides; dt_bias is then (heads).
+ *   a_log         fp32 (heads), and dt_bias fp32 (heads, D) or (heads), contiguous:
+ *                 KDA_GATE_SOFTPLUS only (dt_bias may be NULL: zero); both NULL
+ *                 otherwise.
+ *   beta          (tokens, heads) of beta_dtype, any strides.
+ *   states        fp32; line l, head h is the D x D matrix at l * state_stride[0] +
+ *                 h * state_stride[1], row v contiguous over k, rows contiguous.
+ *                 16-byte aligned, strides multiples of 4. Updated in place.
+ *   cache_indices, has_initial_state, query_start_loc, null_block_id: as for
+ *                 kda_packed_conv1d (a sequence with the null index starts from
+ *                 zero and its state is neither read nor written; without an
+ *                 initial state the line is only written). A sequence of no
+ *                 tokens leaves its line as it was; rows that no sequence owns are
+ *                 left as they were in out.
+ * Token rows are clamped to [0, tokens). A log decay above 0, or a beta * |k|^2
+ * outside [0, 2], makes the recurrence itself grow; it is computed as written.
+ */
+typedef struct kda_delta {
+    int32_t version;          /* 0 */
+    int32_t x_dtype;          /* kda_dtype_t of q, k, v, out */
+    int32_t gate_dtype;       /* kda_dtype_t */
+    int32_t beta_dtype;       /* kda_dtype_t */
+    int32_t gate_kind;        /* kda_gate_t */
+    int32_t gate_per_channel; /* 0 or 1 */
+    int32_t beta_kind;        /* kda_beta_t */
+    int32_t head_dim;         /* 64 or 128 */
+    int64_t heads;
+    float scale;
+    int32_t reserved; /* 0 */
+    const void *q, *k, *v, *gate, *beta;
+    const float *a_log, *dt_bias;
+    float *states;
+    void *out;
+    int64_t q_stride[2], k_stride[2], v_stride[2], gate_stride[2], beta_stride[2], out_stride[2];
+    int64_t state_stride[2];    /* line, head */
+    int64_t cache_index_stride; /* 0 means 1 */
+} kda_delta_t;
+
+/*
+ * kda_packed_delta_rule -- the rule over a packed batch. workspace: device
+ * memory of at least kda_packed_delta_rule_workspace bytes, 256-byte aligned,
+ * not shared with a call that may overlap this one (NULL when that is 0); its
+ * contents need no initialisation and mean nothing afterwards.
+ */
+kda_status_t kda_packed_delta_rule(const kda_delta_t *d, int64_t tokens,
+                                   const int32_t *cache_indices, const uint8_t *has_initial_state,
+                                   const int32_t *query_start_loc, int64_t num_seqs,
+                                   int64_t null_block_id, void *workspace, int64_t workspace_bytes,
+                                   kda_stream_t stream);
+
+/* Bytes of workspace for these sizes on a GPU with sm_count SMs (0: the current
+ * device; a positive sm_count makes no CUDA call). */
+kda_status_t kda_packed_delta_rule_workspace(int64_t tokens, int64_t num_seqs, int64_t heads,
+                                             int32_t head_dim, int32_t x_dtype, int32_t sm_count,
+                                             int64_t *bytes);
+
+/* kda_delta_rule_update -- one token per sequence: row i is the next token of
+ * the sequence at line cache_indices[i]. One launch, no workspace. */
+kda_status_t kda_delta_rule_update(const kda_delta_t *d, int64_t batch,
+                                   const int32_t *cache_indices, int64_t null_block_id,
+                                   kda_stream_t stream);
+
+/* kda_delta_check -- host only: the status the two calls return for this
+ * description (pointers are inspected for NULL and alignment only). */
+kda_status_t kda_delta_check(const kda_delta_t *d);
+
+/*
+ * kda_gated_rmsnorm -- for each row and head of head_dim channels
+ *     out = x / sqrt(mean(x^2) + eps) * weight * act(gate)
+ * in FP32, rounded to nearest even. x, gate, out: (rows, heads, head_dim) of
+ * dtype, channels contiguous, strides {row, head} in elements, 16-byte aligned
+ * with strides multiples of 16 bytes; head_dim a multiple of 16 bytes, at most
+ * 1024 (512 for fp32). weight: fp32 (head_dim) or NULL (ones), 16-byte aligned. gate NULL only
+ * with KDA_NORM_GATE_NONE. out may be x or gate itself; it must not overlap
+ * them in another way. eps >= 0 and finite.
+ */
+kda_status_t kda_gated_rmsnorm(const void *x, const int64_t x_stride[2], const void *gate,
+                               const int64_t gate_stride[2], const float *weight, float eps,
+                               int activation, int64_t rows, int64_t heads, int64_t head_dim,
+                               int dtype, void *out, const int64_t out_stride[2],
+                               kda_stream_t stream);
+
+/*
+ * kda_residual_rmsnorm -- the join between two blocks:
+ *     p = post_weight ? y / sqrt(mean(y^2) + eps) * post_weight : y
+ *     r = residual + scale * act(gate) * p            -> residual_out (rounded)
+ *     out = r / sqrt(mean(r^2) + eps) * weight        (r before rounding)
+ * for each row of `width` channels, in FP32. y, gate, out: (rows, width) of
+ * dtype; residual, residual_out: of dtype or, with residual_f32, fp32. Row
+ * strides in elements; 16-byte aligned, strides multiples of 16 bytes; width a
+ * multiple of 16 bytes of dtype, at most 16384 (8192 for fp32). weight, post_weight: fp32
+ * (width), 16-byte aligned; weight NULL means ones, post_weight NULL no norm of
+ * y. gate NULL only with KDA_NORM_GATE_NONE. residual_out may be residual, and
+ * out may be y or gate; other overlaps are not allowed.
+ */
+kda_status_t kda_residual_rmsnorm(const void *y, int64_t y_stride, const void *residual,
+                                  int64_t residual_stride, const void *gate, int64_t gate_stride,
+                                  const float *weight, const float *post_weight, float scale,
+                                  float eps, int activation, int64_t rows, int64_t width,
+                                  int dtype, int residual_f32, void *out, int64_t out_stride,
+                                  void *residual_out, int64_t residual_out_stride,
+                                  kda_stream_t stream);
+
+/* The CUDA error text behind the calling thread's last KDA_ERR_CUDA from a
+ * function of this header ("" if none). */
+const char *kda_layer_error_string(void);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* KDA_LAYER_H_ */

@@ -49,3 +49,18 @@ from ._binding import (  # noqa: F401
     validate_metadata,
     validate_metadata_device,
 )
+from ._layer import (  # noqa: F401
+    KDA_BETA_PLAIN,
+    KDA_BETA_SIGMOID,
+    KDA_GATE_LOG,
+    KDA_GATE_SOFTPLUS,
+    KDA_NORM_GATE_NONE,
+    KDA_NORM_GATE_SIGMOID,
+    KDA_NORM_GATE_SILU,
+    KdaDelta,
+    delta_rule_update,
+    delta_rule_workspace,
+    gated_rmsnorm,
+    packed_delta_rule_fn,
+    residual_rmsnorm,
+)
