@@ -12,7 +12,7 @@
 // k, q, v, k.q, beta): a warp per token, once for all rows of the block.
 //
 // Bound: for one token the state, read and written once, in HBM.
-#include "kda_delta.cuh"
+#include "kda_delta_chunk.cuh"
 
 namespace kda_layer {
 namespace {
@@ -252,6 +252,12 @@ DeltaParams params_of(const kda_delta_t *d) {
     return p;
 }
 
+// Sequences up to this length go token by token, longer ones in chunks.
+constexpr int kShortLen = 16;
+
+// Whether a packed call uses the chunked path: 16-bit x and sequences that can be long.
+bool uses_chunks(int64_t tokens, int x_dtype) { return x_dtype != KDA_DTYPE_F32 && tokens > kShortLen; }
+
 // Grids of (sequences x heads) blocks, and token rows, stay below 2^31.
 bool sizes_ok(int64_t tokens, int64_t num_seqs, int64_t heads) {
     return tokens >= 0 && num_seqs >= 0 && tokens <= INT32_MAX && num_seqs <= INT32_MAX &&
@@ -274,6 +280,8 @@ kda_status_t kda_packed_delta_rule_workspace(int64_t tokens, int64_t num_seqs, i
         return KDA_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return KDA_ERR_UNSUPPORTED;
     *bytes = 0;
+    if (tokens > 0 && num_seqs > 0 && uses_chunks(tokens, x_dtype))
+        *bytes = chunk_plan(tokens, num_seqs, heads, head_dim, sm_count ? sm_count : current_sms()).bytes;
     return KDA_OK;
 }
 
@@ -294,8 +302,14 @@ kda_status_t kda_packed_delta_rule(const kda_delta_t *d, int64_t tokens,
     p.null_block_id = null_block_id;
     p.num_seqs = (int)num_seqs;
     p.tokens = tokens;
-    (void)workspace, (void)workspace_bytes;
-    return cuda_status(run_recurrent(p, d, INT32_MAX, stream));
+    if (!uses_chunks(tokens, d->x_dtype)) return cuda_status(run_recurrent(p, d, INT32_MAX, stream));
+    const ChunkPlan plan = chunk_plan(tokens, num_seqs, d->heads, d->head_dim, current_sms());
+    if (workspace == nullptr || workspace_bytes < plan.bytes || plan.slots * d->heads > INT32_MAX)
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return KDA_ERR_MISALIGNED;
+    cudaError_t e = run_chunked(p, d, plan, kShortLen, workspace, stream);
+    if (e == cudaSuccess) e = run_recurrent(p, d, kShortLen, stream);
+    return cuda_status(e);
 }
 
 kda_status_t kda_delta_rule_update(const kda_delta_t *d, int64_t batch, const int32_t *cache_indices,
