@@ -53,14 +53,12 @@ __global__ void __launch_bounds__(kWarps * 32)
             S[g][i][0] = f.x, S[g][i][1] = f.y, S[g][i][2] = f.z, S[g][i][3] = f.w;
         }
     }
-    float neg_a = 0.0f, bias[C] = {};
-    if (p.gate_kind == KDA_GATE_SOFTPLUS) {
-        neg_a = -expf(p.a_log[h]);
-        if (p.dt_bias != nullptr)
+    const float factor = gate_factor(p.a_log, h, p.gate_kind);
+    float bias[C] = {};
+    if (p.dt_bias != nullptr)
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                bias[c] = kChannelGate ? p.dt_bias[h * D + lane * C + c] : p.dt_bias[h];
-    }
+        for (int c = 0; c < C; ++c)
+            bias[c] = kChannelGate ? p.dt_bias[h * D + lane * C + c] : p.dt_bias[h];
     for (int64_t base = seq.start; base < seq.end; base += kBatch) {
         const int n = (int)min((int64_t)kBatch, seq.end - base);
         if (base != seq.start) __syncthreads();
@@ -74,10 +72,10 @@ __global__ void __launch_bounds__(kWarps * 32)
             if constexpr (kChannelGate) {
                 const auto gv = ld_vec<G, C>(static_cast<const G *>(p.gate) + t * p.gs[0] + h * p.gs[1] + lane * C);
 #pragma unroll
-                for (int c = 0; c < C; ++c) a[c] = decay_of(to_f<G>(gv.v[c]), p.gate_kind, neg_a, bias[c]);
+                for (int c = 0; c < C; ++c) a[c] = decay_of(to_f<G>(gv.v[c]), p.gate_kind, factor, bias[c]);
             } else {
                 const float one = decay_of(ld_dyn(p.gate, t * p.gs[0] + h * p.gs[1], p.gate_dtype),
-                                           p.gate_kind, neg_a, bias[0]);
+                                           p.gate_kind, factor, bias[0]);
 #pragma unroll
                 for (int c = 0; c < C; ++c) a[c] = one;
             }
@@ -211,7 +209,7 @@ kda_status_t check(const kda_delta_t *d) {
         (d->gate_per_channel != 0 && d->gate_per_channel != 1) || d->heads <= 0 ||
         !isfinite(d->scale) || d->cache_index_stride < 0)
         return KDA_ERR_INVALID_ARG;
-    if ((d->head_dim != 64 && d->head_dim != 128) || d->heads > (1 << 16)) return KDA_ERR_UNSUPPORTED;
+    if ((d->head_dim != 64 && d->head_dim != 128) || d->heads > 65535) return KDA_ERR_UNSUPPORTED;
     if (d->q == nullptr || d->k == nullptr || d->v == nullptr || d->gate == nullptr || d->beta == nullptr ||
         d->states == nullptr || d->out == nullptr)
         return KDA_ERR_INVALID_ARG;

@@ -30,6 +30,8 @@
 // against the 8 or 11 of the output's type.
 #include "kda_delta_chunk.cuh"
 
+#include <type_traits>
+
 namespace kda_layer {
 namespace {
 
@@ -40,10 +42,11 @@ namespace {
 // piece ^ (r % 8), column blocks of 64 one after another.
 template <int D>
 struct Slot {
-    static constexpr int kW = kChunk * D * 2;                 // one W image (hi or lo)
-    static constexpr int w_hi = 0, w_lo = kW;                 // [token][k]
-    static constexpr int k_hi = 2 * kW, k_lo = 3 * kW;        // [k][token]
-    static constexpr int q = 4 * kW;                          // [token][k]
+    static constexpr int kW = kChunk * D * 2;                 // one [token][k] image
+    static constexpr int kRows = 3 * kChunk;                  // rows of the image of q, W hi, W lo
+    static constexpr int kBlock = kRows * 128;                // its column block of 64
+    static constexpr int qw = 0;                              // [q | W hi | W lo token][k]
+    static constexpr int k_hi = 3 * kW, k_lo = 4 * kW;        // [k][token]
     static constexpr int a = 5 * kW;                          // [i][j], 64 x 64
     static constexpr int u = a + kChunk * kChunk * 2;         // fp32 [token][v]
     static constexpr int decay = u + kChunk * D * 4;          // fp32 [k]: G_63
@@ -51,7 +54,9 @@ struct Slot {
     static constexpr int bytes = scales + 64;
 };
 
-constexpr int kHeader = 256;  // workspace: first word set when a wait ran out
+// Head of the workspace, written by the preparation: a word set when a wait ran
+// out, then the item counters of the two walks.
+constexpr int kHeader = 256;
 
 __host__ __device__ constexpr int64_t slot_bytes(int D) { return D == 64 ? Slot<64>::bytes : Slot<128>::bytes; }
 
@@ -79,14 +84,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// hi and lo halves of two values.
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    const __half2 h = __floats2half2_rn(a, b);
-    const float2 f = __half22float2(h);
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    lo = pack2(a - f.x, b - f.y);
-}
-
 // ------------------------------------------------------------------ mma.sync
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
@@ -111,6 +108,51 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], con
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+// m16n8k8 in tf32: A rows (g, t), B columns, as m16n8k16 with 4-byte elements.
+__device__ __forceinline__ void mma8_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+                 "{%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// x = hi + lo to 22 bits, both tf32.
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+
+// c += A B for 16 x 16 FP32 blocks in shared memory (rows lda and ldb floats
+// apart), as three tf32 products: unlike halves these need no scaling.
+__device__ __forceinline__ void block_product(float (&c)[2][4], const float *A, int lda, const float *B,
+                                              int ldb, int lane) {
+    const int g = lane / 4, t = lane % 4;
+#pragma unroll
+    for (int k = 0; k < 16; k += 8) {
+        uint32_t ah[4], al[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            split_tf32(A[(g + i % 2 * 8) * lda + k + t + i / 2 * 4], ah[i], al[i]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) split_tf32(B[(k + t + i * 4) * ldb + n * 8 + g], bh[i], bl[i]);
+            mma8_tf32(c[n], ah, bh);
+            mma8_tf32(c[n], al, bh);
+            mma8_tf32(c[n], ah, bl);
+        }
+    }
+}
+__device__ __forceinline__ void block_store(float *to, int ld, const float (&c)[2][4], float sign, int lane) {
+    const int g = lane / 4, t = lane % 4 * 2;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+            *reinterpret_cast<float2 *>(to + (g + e * 4) * ld + n * 8 + t) =
+                make_float2(sign * c[n][e], sign * c[n][e + 1]);
+}
+
 // ------------------------------------------------------------------ prepare
 
 // The sequence that owns slot j of a map f(s) = floor(qsl[s] / unit) + s (the
@@ -127,6 +169,22 @@ __device__ __forceinline__ int find_seq(const DeltaParams &p, int64_t j, int64_t
     return lo;
 }
 
+// The same for unit kChunk by a whole block of 256 threads: each round narrows
+// the range 256-fold with one load per thread.
+__device__ __forceinline__ int find_seq_block(const DeltaParams &p, int64_t j, int64_t &rest) {
+    int lo = 0, n = p.num_seqs;
+    while (n > 1) {
+        const int step = (n + 255) / 256, i = (int)threadIdx.x * step;
+        bool below = false;
+        if (i < n) below = max(p.query_start_loc[lo + i], 0) / kChunk + lo + i <= j;
+        const int count = max(__syncthreads_count(below), 1);
+        lo += (count - 1) * step;
+        n = min(step, n - (count - 1) * step);
+    }
+    rest = j - (max(p.query_start_loc[lo], 0) / kChunk + lo);
+    return lo;
+}
+
 template <int D>
 struct PrepSmem {
     static constexpr int kRow = D + 8;  // halves: rows 16 bytes past a multiple of 128 bytes
@@ -140,28 +198,49 @@ struct PrepSmem {
         struct { __half hi[64][72], lo[64][72]; } t;
     } l;
     float T[64][68];
-    float tmp[3][16][20];
+    float tmp[4][16][20];
     __half A[64][72];
     float block_decay[8][D];
     float beta[64];
-    uint32_t top[4][8];  // per warp: largest |k|, |q|, |v|, then T', W
+    uint32_t top[4][8];  // per warp: largest |k| (then W), |q|, |v|, T'
 };
 
-template <int C>
-__device__ __forceinline__ void store_row(__half *at, const float (&f)[C]) {
-    if constexpr (C == 4) {
-        *reinterpret_cast<uint2 *>(at) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
-    } else {
-        *reinterpret_cast<uint32_t *>(at) = pack2(f[0], f[1]);
+// Pairs of channels: FP32 in both halves of a 64-bit register pair.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+// decay_of for two channels.
+__device__ __forceinline__ float2 decay2_of(float2 raw, int kind, float factor, float2 bias) {
+    float2 x = raw;
+    if (kind == KDA_GATE_SOFTPLUS) {
+        x = __fadd2_rn(raw, bias);
+        const float2 e = make_float2(exp2_f(fabsf(x.x) * -1.4426950408889634f), exp2_f(fabsf(x.y) * -1.4426950408889634f));
+        x = softplus_tail2(e, make_float2(fmaxf(x.x, 0.0f), fmaxf(x.y, 0.0f)));
     }
+    x = mul2(x, make_float2(factor, factor));
+    return make_float2(exp2_f(x.x), exp2_f(x.y));
 }
 
-template <int C>
-__device__ __forceinline__ void store_split(__half *hi, __half *lo, const float (&f)[C]) {
+__device__ __forceinline__ void split2(float2 f, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __float22half2_rn(f);
+    const float2 g = __half22float2(h);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    const __half2 l = __float22half2_rn(fma2(g, make_float2(-1.0f, -1.0f), f));
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+__device__ __forceinline__ uint32_t pack2(float2 f) { return pack2(f.x, f.y); }
+
+template <int P>
+__device__ __forceinline__ void store_row(void *at, const float2 (&f)[P]) {
+    if constexpr (P == 2) *reinterpret_cast<uint2 *>(at) = make_uint2(pack2(f[0]), pack2(f[1]));
+    else *reinterpret_cast<uint32_t *>(at) = pack2(f[0]);
+}
+template <int P>
+__device__ __forceinline__ void store_split(__half *hi, __half *lo, const float2 (&f)[P]) {
     uint32_t h[2], l[2];
-    split2(f[0], f[1], h[0], l[0]);
-    if constexpr (C == 4) {
-        split2(f[2], f[3], h[1], l[1]);
+    split2(f[0], h[0], l[0]);
+    if constexpr (P == 2) {
+        split2(f[1], h[1], l[1]);
         *reinterpret_cast<uint2 *>(hi) = make_uint2(h[0], h[1]);
         *reinterpret_cast<uint2 *>(lo) = make_uint2(l[0], l[1]);
     } else {
@@ -170,22 +249,50 @@ __device__ __forceinline__ void store_split(__half *hi, __half *lo, const float 
     }
 }
 
-// The sums over the warp of 32 values, value i to lane i.
-__device__ __forceinline__ float scatter_sum(float (&v)[32], int lane) {
+// The sums over the warp of 16 values, value i to lanes 2 i and 2 i + 1.
+__device__ __forceinline__ float scatter_sum(float (&v)[16], int lane) {
 #pragma unroll
-    for (int m = 16; m > 0; m /= 2) {
+    for (int m = 16; m > 1; m /= 2) {
         const bool up = lane & m;
 #pragma unroll
-        for (int i = 0; i < m; ++i) {
-            const float send = up ? v[i] : v[i + m];
-            const float keep = up ? v[i + m] : v[i];
+        for (int i = 0; i < m / 2; ++i) {
+            const float send = up ? v[i] : v[i + m / 2];
+            const float keep = up ? v[i + m / 2] : v[i];
             v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
         }
     }
-    return v[0];
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// The larger of 8 warps' bit patterns of magnitudes, as a float.
+// Keeps the compiler from carrying the FP32 forms of packed halves from one stage
+// to the next, which would not fit in the registers.
+template <typename X>
+__device__ __forceinline__ void repack(X (&x)[8]) {
+    constexpr int N = sizeof(X) / 4;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int c = 0; c < N; ++c) asm volatile("" : "+r"(reinterpret_cast<uint32_t *>(&x[r])[c]));
+}
+
+__device__ __forceinline__ __half low_of(__half2 x) { return __low2half(x); }
+__device__ __forceinline__ __half high_of(__half2 x) { return __high2half(x); }
+__device__ __forceinline__ __nv_bfloat16 low_of(__nv_bfloat162 x) { return __low2bfloat16(x); }
+__device__ __forceinline__ __nv_bfloat16 high_of(__nv_bfloat162 x) { return __high2bfloat16(x); }
+
+// The largest magnitude of 8 rows of 16-bit values.
+template <typename T, int C>
+__device__ __forceinline__ float max_of(const Vec<T, C> (&x)[8]) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    T2 m = __habs2(*reinterpret_cast<const T2 *>(&x[0].v[0]));
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int c = 0; c < C; c += 2) m = __hmax2(m, __habs2(*reinterpret_cast<const T2 *>(&x[r].v[c])));
+    return fmaxf(to_f<T>(low_of(m)), to_f<T>(high_of(m)));
+}
+
+// The largest of 8 warps' bit patterns of magnitudes, as a float.
 __device__ __forceinline__ float top_of(const uint32_t (&t)[8]) {
     uint32_t m = t[0];
 #pragma unroll
@@ -200,14 +307,15 @@ __device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0
 template <typename T, int D, bool kChannelGate, typename G>
 __global__ void __launch_bounds__(256, 2)
     delta_prepare_kernel(const __grid_constant__ DeltaParams p, char *ws, int short_len) {
-    constexpr int C = D / 32;
+    constexpr int C = D / 32, P = C / 2;
     extern __shared__ __align__(1024) char raw_smem[];
     PrepSmem<D> &sm = *reinterpret_cast<PrepSmem<D> *>(raw_smem);
     dependency_wait();
+    if (blockIdx.x == 0 && threadIdx.x < 3) reinterpret_cast<int *>(ws)[threadIdx.x] = 0;
     const int64_t slot = blockIdx.x / p.heads;
     const int h = blockIdx.x % p.heads;
     int64_t chunk;
-    const int s = find_seq(p, slot, kChunk, chunk);
+    const int s = find_seq_block(p, slot, chunk);
     const Seq seq = load_seq(p, s);
     const int64_t len = seq.end - seq.start;
     if (len <= short_len || chunk < 0 || chunk * kChunk >= len) return;
@@ -216,185 +324,173 @@ __global__ void __launch_bounds__(256, 2)
     const int b = threadIdx.x / 32, lane = threadIdx.x % 32;
     char *out = ws + kHeader + (slot * p.heads + h) * slot_bytes(D);
 
-    // ---- load; rows past the sequence's end are k = q = v = beta = 0, decay 1
-    float k[8][C], q[8][C], a[8][C];
-    Vec<T, C> vraw[8];
+    // ---- load; rows past the sequence's end are k = q = v = beta = 0, decay 1.
+    // k and q stay as halves scaled by a power of two (exact but for values
+    // below 2^-29 of the tile's largest), which halves their registers.
+    __half2 k[8][P], q[8][P];
+    float2 a[8][P];
+    float down_k, down_q, down_v;
     {
-        float neg_a = 0.0f, bias[C] = {};
-        if (p.gate_kind == KDA_GATE_SOFTPLUS) {
-            neg_a = -expf(p.a_log[h]);
-            if (p.dt_bias != nullptr)
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-                    bias[c] = kChannelGate ? p.dt_bias[h * D + lane * C + c] : p.dt_bias[h];
-        }
+        const T *kp = static_cast<const T *>(p.k) + (t0 + b * 8) * p.ks[0] + h * p.ks[1] + lane * C;
+        const T *qp = static_cast<const T *>(p.q) + (t0 + b * 8) * p.qs[0] + h * p.qs[1] + lane * C;
+        const T *vp = static_cast<const T *>(p.v) + (t0 + b * 8) * p.vs[0] + h * p.vs[1] + lane * C;
+        Vec<T, C> kv[8], qv[8], vv[8];
+        Vec<G, C> gv[8];
+        float one[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            const int64_t t = t0 + b * 8 + r;
-            const bool in = b * 8 + r < n;
-            if (in) {
-                const auto kv = ld_vec<T, C>(static_cast<const T *>(p.k) + t * p.ks[0] + h * p.ks[1] + lane * C);
-                const auto qv = ld_vec<T, C>(static_cast<const T *>(p.q) + t * p.qs[0] + h * p.qs[1] + lane * C);
-                vraw[r] = ld_vec<T, C>(static_cast<const T *>(p.v) + t * p.vs[0] + h * p.vs[1] + lane * C);
-                if constexpr (kChannelGate) {
-                    const auto gv = ld_vec<G, C>(static_cast<const G *>(p.gate) + t * p.gs[0] + h * p.gs[1] + lane * C);
-#pragma unroll
-                    for (int c = 0; c < C; ++c) a[r][c] = to_f<G>(gv.v[c]);
-                } else {
-                    const float one = ld_dyn(p.gate, t * p.gs[0] + h * p.gs[1], p.gate_dtype);
-#pragma unroll
-                    for (int c = 0; c < C; ++c) a[r][c] = one;
-                }
-#pragma unroll
-                for (int c = 0; c < C; ++c) k[r][c] = to_f<T>(kv.v[c]), q[r][c] = to_f<T>(qv.v[c]);
+            one[r] = 0.0f;
+            if (b * 8 + r < n) {
+                if constexpr (kChannelGate)
+                    gv[r] = ld_vec<G, C>(static_cast<const G *>(p.gate) + (t0 + b * 8 + r) * p.gs[0] + h * p.gs[1] + lane * C);
+                else
+                    one[r] = ld_dyn(p.gate, (t0 + b * 8 + r) * p.gs[0] + h * p.gs[1], p.gate_dtype);
+                kv[r] = ld_vec<T, C>(kp + r * p.ks[0]);
+                qv[r] = ld_vec<T, C>(qp + r * p.qs[0]);
+                vv[r] = ld_vec<T, C>(vp + r * p.vs[0]);
             } else {
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    k[r][c] = q[r][c] = a[r][c] = 0.0f;
-                    vraw[r].v[c] = from_f<T>(0.0f);
+                    kv[r].v[c] = qv[r].v[c] = vv[r].v[c] = from_f<T>(0.0f);
+                    if constexpr (kChannelGate) gv[r].v[c] = from_f<G>(0.0f);
                 }
             }
         }
+        if (lane < 8) {
+            const int64_t t = t0 + b * 8 + lane;
+            sm.beta[b * 8 + lane] =
+                b * 8 + lane < n ? beta_of(ld_dyn(p.beta, t * p.bs[0] + h * p.bs[1], p.beta_dtype), p.beta_kind) : 0.0f;
+        }
+        const float factor = gate_factor(p.a_log, h, p.gate_kind);
+        float bias[C] = {};
+        if (p.dt_bias != nullptr)
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
+            for (int c = 0; c < C; ++c) bias[c] = kChannelGate ? p.dt_bias[h * D + lane * C + c] : p.dt_bias[h];
+        float2 whole[P];
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                a[r][c] = b * 8 + r < n ? decay_of(a[r][c], p.gate_kind, neg_a, bias[c]) : 1.0f;
-    }
-    if (lane < 8) {
-        const int64_t t = t0 + b * 8 + lane;
-        sm.beta[b * 8 + lane] =
-            b * 8 + lane < n ? beta_of(ld_dyn(p.beta, t * p.bs[0] + h * p.bs[1], p.beta_dtype), p.beta_kind) : 0.0f;
-    }
-    {
-        uint32_t mk = 0, mq = 0, mv = 0;
-        float whole[C];
+        for (int c = 0; c < P; ++c) whole[c] = make_float2(1.0f, 1.0f);
 #pragma unroll
-        for (int c = 0; c < C; ++c) whole[c] = 1.0f;
+        for (int r = 0; r < 8; ++r) {
+            const bool in = b * 8 + r < n;
+            const float same = kChannelGate || !in ? 1.0f : decay_of(one[r], p.gate_kind, factor, bias[0]);
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                mk = max(mk, mag(k[r][c])), mq = max(mq, mag(q[r][c]));
-                mv = max(mv, mag(to_f<T>(vraw[r].v[c])));
-                whole[c] *= a[r][c];
+            for (int c = 0; c < P; ++c) {
+                a[r][c] = make_float2(same, same);
+                if constexpr (kChannelGate) {
+                    a[r][c] = decay2_of(make_float2(to_f<G>(gv[r].v[2 * c]), to_f<G>(gv[r].v[2 * c + 1])), p.gate_kind,
+                                        factor, make_float2(bias[2 * c], bias[2 * c + 1]));
+                    if (!in) a[r][c] = make_float2(1.0f, 1.0f);
+                }
+                whole[c] = mul2(whole[c], a[r][c]);
             }
-        mk = __reduce_max_sync(0xffffffffu, mk);
-        mq = __reduce_max_sync(0xffffffffu, mq);
-        mv = __reduce_max_sync(0xffffffffu, mv);
-        if (lane == 0) sm.top[0][b] = mk, sm.top[1][b] = mq, sm.top[2][b] = mv;
+        }
 #pragma unroll
-        for (int c = 0; c < C; ++c) sm.block_decay[b][lane * C + c] = whole[c];
+        for (int c = 0; c < P; ++c)
+            *reinterpret_cast<float2 *>(&sm.block_decay[b][lane * C + 2 * c]) = whole[c];
+        const uint32_t wk = __reduce_max_sync(0xffffffffu, mag(max_of<T, C>(kv))),
+                       wq = __reduce_max_sync(0xffffffffu, mag(max_of<T, C>(qv))),
+                       wv = __reduce_max_sync(0xffffffffu, mag(max_of<T, C>(vv)));
+        repack(kv), repack(qv), repack(vv);
+        if (lane == 0) sm.top[0][b] = wk, sm.top[1][b] = wq, sm.top[2][b] = wv;
+        // T's blocks above the diagonal and A's elements above it are zeros.
+        for (int i = threadIdx.x; i < 64 * 68 / 4; i += 256)
+            reinterpret_cast<float4 *>(&sm.T[0][0])[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i = threadIdx.x; i < 64 * 72 / 8; i += 256)
+            reinterpret_cast<uint4 *>(&sm.A[0][0])[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        const float top_k = top_of(sm.top[0]), top_q = top_of(sm.top[1]), top_v = top_of(sm.top[2]);
+        down_k = scale_down(top_k), down_q = scale_down(top_q), down_v = scale_down(top_v);
+        const float up_k = scale_up(top_k), up_q = scale_up(top_q), up_v = scale_up(top_v);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            float2 f[P];
+#pragma unroll
+            for (int c = 0; c < P; ++c) {
+                k[r][c] = __floats2half2_rn(to_f<T>(kv[r].v[2 * c]) * up_k, to_f<T>(kv[r].v[2 * c + 1]) * up_k);
+                q[r][c] = __floats2half2_rn(to_f<T>(qv[r].v[2 * c]) * up_q, to_f<T>(qv[r].v[2 * c + 1]) * up_q);
+                f[c] = make_float2(to_f<T>(vv[r].v[2 * c]) * up_v, to_f<T>(vv[r].v[2 * c + 1]) * up_v);
+            }
+            store_row<P>(&sm.v[b * 8 + r][lane * C], f);
+        }
     }
-    // L and A start as zeros (L's upper part is read by the block products).
-    for (int i = threadIdx.x; i < 64 * 68; i += 256) (&sm.l.L[0][0])[i] = 0.0f, (&sm.T[0][0])[i] = 0.0f;
-    for (int i = threadIdx.x; i < 64 * 72 / 2; i += 256) reinterpret_cast<uint32_t *>(&sm.A[0][0])[i] = 0;
-    __syncthreads();
-    const float top_k = top_of(sm.top[0]), top_q = top_of(sm.top[1]), top_v = top_of(sm.top[2]);
-    const float up_k = scale_up(top_k), up_q = scale_up(top_q), up_v = scale_up(top_v);
-    const float down_k = scale_down(top_k), down_q = scale_down(top_q), down_v = scale_down(top_v);
-    // |A| < 2^(e_q + e_k + 9), so A up_q up_k 2^-22 is below 2^15.
-    const float up_a = up_q * 0x1p-11f, up_a2 = up_k * 0x1p-11f;
+    // A is kept as A up_q up_k 2^-22, below 2^15 since |A| < 2^(e_q + e_k + 9).
+    constexpr float kDownA = 0x1p-22f;
+    const float down_kk = down_k * down_k;
 
-    // ---- pairs inside 8 tokens: running products of decays, FP32
+    // ---- pairs inside 8 tokens: running products of decays, FP32. For j = 0..7:
+    // q_j k_j, then for i > j the pair (k_i k_j, q_i k_j); 64 sums in batches of 16.
     {
-        const int at = lane;
-        const int i = 1 + (at >= 1) + (at >= 3) + (at >= 6) + (at >= 10) + (at >= 15) + (at >= 21);
-        const int j = at - i * (i - 1) / 2;
-        float f[32];
+        repack(k), repack(q);
+        float f[16];
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {
-            float w[C];
+            const int first = jj * (16 - jj);
+            float2 w[P];
 #pragma unroll
-            for (int c = 0; c < C; ++c) w[c] = k[jj][c];
+            for (int ii = jj; ii < 8; ++ii) {
+                float2 sk = make_float2(0.0f, 0.0f), sq = sk;
 #pragma unroll
-            for (int ii = jj + 1; ii < 8; ++ii) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    w[c] *= a[ii][c];
-                    sum = fmaf(k[ii][c], w[c], sum);
+                for (int c = 0; c < P; ++c) {
+                    w[c] = ii == jj ? __half22float2(k[jj][c]) : mul2(w[c], a[ii][c]);
+                    const float2 ki = __half22float2(k[ii][c]), qi = __half22float2(q[ii][c]);
+                    if (ii > jj) sk = c == 0 ? mul2(ki, w[c]) : fma2(ki, w[c], sk);
+                    sq = c == 0 ? mul2(qi, w[c]) : fma2(qi, w[c], sq);
                 }
-                f[ii * (ii - 1) / 2 + jj] = sum;
+#pragma unroll
+                for (int what = 0; what < 2; ++what) {
+                    if (ii == jj && what == 0) continue;
+                    const int at = first + 2 * (ii - jj) - 1 + what;  // 2 (i - j) - 1: k, 2 (i - j): q
+                    f[at % 16] = what ? sq.x + sq.y : sk.x + sk.y;
+                    if (at % 16 == 15) {
+                        const float got = scatter_sum(f, lane);
+                        const int mine = at - 15 + lane / 2;
+                        const int j = (mine >= 15) + (mine >= 28) + (mine >= 39) + (mine >= 48) +
+                                      (mine >= 55) + (mine >= 60) + (mine >= 63);
+                        const int e = mine - j * (16 - j), i = j + (e + 1) / 2;
+                        if (e % 2 == 1) sm.l.L[b * 8 + i][b * 8 + j] = got * down_kk * sm.beta[b * 8 + i];
+                        else sm.A[b * 8 + i][b * 8 + j] = __float2half_rn(got * kDownA);
+                    }
+                }
             }
         }
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            f[28 + d] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < C; ++c) f[28 + d] = fmaf(q[d][c], k[d][c], f[28 + d]);
-        }
-        float got = scatter_sum(f, lane);
-        if (lane < 28) sm.l.L[b * 8 + i][b * 8 + j] = got * sm.beta[b * 8 + i];
-        else sm.A[b * 8 + lane - 28][b * 8 + lane - 28] = __float2half_rn(got * up_a * up_a2);
-#pragma unroll
-        for (int jj = 0; jj < 8; ++jj) {
-            float w[C];
-#pragma unroll
-            for (int c = 0; c < C; ++c) w[c] = k[jj][c];
-#pragma unroll
-            for (int ii = jj + 1; ii < 8; ++ii) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    w[c] *= a[ii][c];
-                    sum = fmaf(q[ii][c], w[c], sum);
-                }
-                f[ii * (ii - 1) / 2 + jj] = sum;
-            }
-        }
-#pragma unroll
-        for (int d = 4; d < 8; ++d) {
-            f[24 + d] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < C; ++c) f[24 + d] = fmaf(q[d][c], k[d][c], f[24 + d]);
-        }
-        got = scatter_sum(f, lane) * up_a * up_a2;
-        if (lane < 28) sm.A[b * 8 + i][b * 8 + j] = __float2half_rn(got);
-        else sm.A[b * 8 + lane - 24][b * 8 + lane - 24] = __float2half_rn(got);
     }
-
-#pragma unroll
-    for (int r = 0; r < 8; ++r)
-#pragma unroll
-        for (int c = 0; c < C; ++c) k[r][c] *= up_k, q[r][c] *= up_q;
 
     // ---- pairs of blocks: per level, the later half's tokens carry the decays
     // from the middle to them, the earlier half's those from them to the middle
     const int g = lane / 4, cc = lane % 4 * 2;
 #pragma unroll 1
     for (int half = 1; half <= 4; half *= 2) {  // blocks of 8 in half a level: 1, 2, 4
+        repack(k), repack(q);
         const int pos = b % (2 * half);         // block's place in its level group
         const int row0 = b / (2 * half) * (half * 8) + (pos % half) * 8;
-        float run[C];
+        float2 run[P];
 #pragma unroll
-        for (int c = 0; c < C; ++c) run[c] = 1.0f;
-        if (pos >= half) {
-            for (int o = half; o < pos; ++o)
+        for (int c = 0; c < P; ++c) run[c] = make_float2(1.0f, 1.0f);
+        const bool later = pos >= half;
+        for (int o = later ? half : pos + 1; o < (later ? pos : half); ++o)
 #pragma unroll
-                for (int c = 0; c < C; ++c) run[c] *= sm.block_decay[b - pos + o][lane * C + c];
+            for (int c = 0; c < P; ++c)
+                run[c] = mul2(run[c], *reinterpret_cast<const float2 *>(&sm.block_decay[b - pos + o][lane * C + 2 * c]));
+        if (later) {
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                float f[C], fq[C];
+                float2 f[P], fq[P];
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    run[c] *= a[r][c];
-                    f[c] = k[r][c] * run[c];
-                    fq[c] = q[r][c] * run[c];
+                for (int c = 0; c < P; ++c) {
+                    run[c] = mul2(run[c], a[r][c]);
+                    f[c] = mul2(__half22float2(k[r][c]), run[c]);
+                    fq[c] = mul2(__half22float2(q[r][c]), run[c]);
                 }
-                store_split<C>(&sm.x.lv.lk_hi[row0 + r][lane * C], &sm.x.lv.lk_lo[row0 + r][lane * C], f);
-                store_row<C>(&sm.x.lv.lq[row0 + r][lane * C], fq);
+                store_split<P>(&sm.x.lv.lk_hi[row0 + r][lane * C], &sm.x.lv.lk_lo[row0 + r][lane * C], f);
+                store_row<P>(&sm.x.lv.lq[row0 + r][lane * C], fq);
             }
         } else {
-            for (int o = pos + 1; o < half; ++o)
-#pragma unroll
-                for (int c = 0; c < C; ++c) run[c] *= sm.block_decay[b - pos + o][lane * C + c];
 #pragma unroll
             for (int r = 7; r >= 0; --r) {
-                float f[C];
+                float2 f[P];
 #pragma unroll
-                for (int c = 0; c < C; ++c) f[c] = k[r][c] * run[c], run[c] *= a[r][c];
-                store_split<C>(&sm.x.lv.rk_hi[row0 + r][lane * C], &sm.x.lv.rk_lo[row0 + r][lane * C], f);
+                for (int c = 0; c < P; ++c) f[c] = mul2(__half22float2(k[r][c]), run[c]), run[c] = mul2(run[c], a[r][c]);
+                store_split<P>(&sm.x.lv.rk_hi[row0 + r][lane * C], &sm.x.lv.rk_lo[row0 + r][lane * C], f);
             }
         }
         __syncthreads();
@@ -420,16 +516,16 @@ __global__ void __launch_bounds__(256, 2)
                     mma16(c, ah, bl);
                 }
                 const int i = b * 16 + 8 + g, j = b * 16 + cc;
-                const float f = sm.beta[i];
+                const float f = sm.beta[i] * down_kk;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    sm.l.L[i][j + e] = c[e] * down_k * down_k * f;
-                    sm.A[i][j + e] = __float2half_rn(c[2 + e] * 0x1p-22f);
+                    sm.l.L[i][j + e] = c[e] * f;
+                    sm.A[i][j + e] = __float2half_rn(c[2 + e] * kDownA);
                 }
             }
         } else {
             const bool wide = half == 4;
-            const int m = wide ? b / 4 : b / 4;               // 16-row tile of the left operand
+            const int m = b / 4;                              // 16-row tile of the left operand
             const int nt = wide ? b % 4 : m * 2 + b / 2 % 2;  // 8-row tile of the right operand
             const bool do_k = wide || b % 2 == 0, do_q = wide || b % 2 == 1;
             float ck[4] = {}, cq[4] = {};
@@ -459,51 +555,79 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = i0 + g + e / 2 * 8, j = j0 + cc + e % 2;
-                if (do_k) sm.l.L[i][j] = ck[e] * down_k * down_k * sm.beta[i];
-                if (do_q) sm.A[i][j] = __float2half_rn(cq[e] * 0x1p-22f);
+                if (do_k) sm.l.L[i][j] = ck[e] * (down_kk * sm.beta[i]);
+                if (do_q) sm.A[i][j] = __float2half_rn(cq[e] * kDownA);
             }
         }
         __syncthreads();
     }
 
+    // ---- T = (I + L)^-1, diagonal blocks of 16 by forward substitution, a column per lane
+    if (b < 4 && lane < 16) {
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int m = 0; m < i; m += 4) {
+                const float4 l = *reinterpret_cast<const float4 *>(&sm.l.L[b * 16 + i][b * 16 + m]);
+                sum = fmaf(l.x, x[m], sum);
+                if (m + 1 < i) sum = fmaf(l.y, x[m + 1], sum);
+                if (m + 2 < i) sum = fmaf(l.z, x[m + 2], sum);
+                if (m + 3 < i) sum = fmaf(l.w, x[m + 3], sum);
+            }
+            x[i] = (i == lane ? 1.0f : 0.0f) - sum;
+            sm.T[b * 16 + i][b * 16 + lane] = x[i];
+        }
+    }
+
     // ---- decays from the chunk's start (k G, q G) and to its end (k G_63 / G)
     {
-        float run[C];
+        repack(k), repack(q);
+        float2 run[P];
 #pragma unroll
-        for (int c = 0; c < C; ++c) run[c] = 1.0f;
+        for (int c = 0; c < P; ++c) run[c] = make_float2(1.0f, 1.0f);
         for (int o = 0; o < b; ++o)
 #pragma unroll
-            for (int c = 0; c < C; ++c) run[c] *= sm.block_decay[o][lane * C + c];
+            for (int c = 0; c < P; ++c)
+                run[c] = mul2(run[c], *reinterpret_cast<const float2 *>(&sm.block_decay[o][lane * C + 2 * c]));
+        // row 8 b + r of the image: its 16-byte piece is at piece ^ r
+        char *qo = out + Slot<D>::qw + (lane * C >> 6) * Slot<D>::kBlock + b * 8 * 128 + (lane * C & 7) * 2;
+        const int piece = lane * C >> 3 & 7;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            float f[C], fq[C], fv[C];
+            float2 f[P], fq[P];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                run[c] *= a[r][c];
-                f[c] = k[r][c] * run[c];
-                fq[c] = q[r][c] * run[c];
-                fv[c] = to_f<T>(vraw[r].v[c]) * up_v;
+            for (int c = 0; c < P; ++c) {
+                run[c] = mul2(run[c], a[r][c]);
+                f[c] = mul2(__half22float2(k[r][c]), run[c]);
+                fq[c] = mul2(__half22float2(q[r][c]), run[c]);
             }
-            const int row = b * 8 + r;
-            store_split<C>(&sm.x.kg.k_hi[row][lane * C], &sm.x.kg.k_lo[row][lane * C], f);
-            store_row<C>(&sm.v[row][lane * C], fv);
-            store_row<C>(reinterpret_cast<__half *>(out + Slot<D>::q + image_at(row, lane * C, 64)), fq);
+            store_split<P>(&sm.x.kg.k_hi[b * 8 + r][lane * C], &sm.x.kg.k_lo[b * 8 + r][lane * C], f);
+            store_row<P>(qo + r * 128 + ((piece ^ r) << 4), fq);
         }
+        if (b == 7)
 #pragma unroll
-        for (int c = 0; c < C; ++c) run[c] = 1.0f;
+            for (int c = 0; c < P; ++c)
+                *reinterpret_cast<float2 *>(out + Slot<D>::decay + (lane * C + 2 * c) * 4) = run[c];
+#pragma unroll
+        for (int c = 0; c < P; ++c) run[c] = make_float2(1.0f, 1.0f);
         for (int o = b + 1; o < 8; ++o)
 #pragma unroll
-            for (int c = 0; c < C; ++c) run[c] *= sm.block_decay[o][lane * C + c];
+            for (int c = 0; c < P; ++c)
+                run[c] = mul2(run[c], *reinterpret_cast<const float2 *>(&sm.block_decay[o][lane * C + 2 * c]));
+        repack(k);
         uint32_t kh[C][4], kl[C][4];
 #pragma unroll
         for (int r = 6; r >= 0; r -= 2)
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const float later = k[r + 1][c] * run[c];
-                run[c] *= a[r + 1][c];
-                const float earlier = k[r][c] * run[c];
-                run[c] *= a[r][c];
-                split2(earlier, later, kh[c][r / 2], kl[c][r / 2]);
+            for (int c = 0; c < P; ++c) {
+                const float2 later = mul2(__half22float2(k[r + 1][c]), run[c]);
+                run[c] = mul2(run[c], a[r + 1][c]);
+                const float2 earlier = mul2(__half22float2(k[r][c]), run[c]);
+                run[c] = mul2(run[c], a[r][c]);
+                split2(make_float2(earlier.x, later.x), kh[2 * c][r / 2], kl[2 * c][r / 2]);
+                split2(make_float2(earlier.y, later.y), kh[2 * c + 1][r / 2], kl[2 * c + 1][r / 2]);
             }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -511,90 +635,86 @@ __global__ void __launch_bounds__(256, 2)
             *reinterpret_cast<uint4 *>(out + Slot<D>::k_hi + at) = make_uint4(kh[c][0], kh[c][1], kh[c][2], kh[c][3]);
             *reinterpret_cast<uint4 *>(out + Slot<D>::k_lo + at) = make_uint4(kl[c][0], kl[c][1], kl[c][2], kl[c][3]);
         }
-        if (b == 0)
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float whole = 1.0f;
-                for (int o = 0; o < 8; ++o) whole *= sm.block_decay[o][lane * C + c];
-                reinterpret_cast<float *>(out + Slot<D>::decay)[lane * C + c] = whole;
-            }
         // A: 64 x 64 halves, two 16-byte pieces per thread
-        for (int i = threadIdx.x; i < 64 * 8; i += 256)
-            *reinterpret_cast<uint4 *>(out + Slot<D>::a + image_at(i / 8, i % 8 * 8, 64)) =
-                *reinterpret_cast<const uint4 *>(&sm.A[i / 8][i % 8 * 8]);
-    }
-
-    // ---- T = (I + L)^-1: 16 x 16 diagonal blocks by forward substitution (a
-    // column per lane), the others from T_IJ = -T_II sum_M L_IM T_MJ
-    if (b < 4 && lane < 16) {
-        float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int m = 0; m < i; ++m) sum = fmaf(sm.l.L[b * 16 + i][b * 16 + m], x[m], sum);
-            x[i] = (i == lane ? 1.0f : 0.0f) - sum;
+        for (int i = 0; i < 2; ++i) {
+            const int row = threadIdx.x / 8 + i * 32, col = threadIdx.x % 8;
+            *reinterpret_cast<uint4 *>(out + Slot<D>::a + row * 128 + ((col ^ (row & 7)) << 4)) =
+                *reinterpret_cast<const uint4 *>(&sm.A[row][col * 8]);
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sm.T[b * 16 + i][b * 16 + lane] = x[i];
     }
     __syncthreads();
-    {
-        const int i = threadIdx.x / 16, j = threadIdx.x % 16;
-#pragma unroll 1
-        for (int dist = 1; dist < 4; ++dist) {
-            for (int J = 0; J + dist < 4; ++J) {
-                const int I = J + dist;
-                float sum = 0.0f;
-                for (int m = J * 16; m < I * 16; ++m) sum = fmaf(sm.l.L[I * 16 + i][m], sm.T[m][J * 16 + j], sum);
-                sm.tmp[J][i][j] = sum;
-            }
-            __syncthreads();
-            for (int J = 0; J + dist < 4; ++J) {
-                const int I = J + dist;
-                float sum = 0.0f;
-#pragma unroll
-                for (int m = 0; m < 16; ++m) sum = fmaf(sm.T[I * 16 + i][I * 16 + m], sm.tmp[J][m][j], sum);
-                sm.T[I * 16 + i][J * 16 + j] = -sum;
-            }
-            __syncthreads();
-        }
+
+    // ---- T below its diagonal blocks: [X 0; Y Z]^-1 = [X^-1 0; -Z^-1 Y X^-1 Z^-1], for
+    // pairs of 16 x 16 blocks, then of 32 x 32
+    if (b < 2) {
+        const int J = 2 * b * 16, I = J + 16;
+        float c[2][4] = {}, d[2][4] = {};
+        block_product(c, &sm.l.L[I][J], 68, &sm.T[J][J], 68, lane);
+        block_store(&sm.tmp[b][0][0], 20, c, 1.0f, lane);
+        __syncwarp();
+        block_product(d, &sm.T[I][I], 68, &sm.tmp[b][0][0], 20, lane);
+        block_store(&sm.T[I][J], 68, d, -1.0f, lane);
     }
+    __syncthreads();
+    if (b < 4) {
+        const int I = b / 2, J = b % 2;
+        float c[2][4] = {};
+        for (int m = J; m < 2; ++m)
+            block_product(c, &sm.l.L[32 + I * 16][m * 16], 68, &sm.T[m * 16][J * 16], 68, lane);
+        block_store(&sm.tmp[b][0][0], 20, c, 1.0f, lane);
+    }
+    __syncthreads();
+    if (b < 4) {
+        const int I = b / 2, J = b % 2;
+        float c[2][4] = {};
+        for (int m = 0; m <= I; ++m)
+            block_product(c, &sm.T[32 + I * 16][32 + m * 16], 68, &sm.tmp[m * 2 + J][0][0], 20, lane);
+        block_store(&sm.T[32 + I * 16][J * 16], 68, c, -1.0f, lane);
+    }
+    __syncthreads();
 
     // ---- W = T diag(beta) k G and U = T diag(beta) v
     {
-        float t[16];
+        float4 t[4];
         uint32_t m = 0;
         const int row = threadIdx.x / 4, col = threadIdx.x % 4 * 16;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            t[i] = sm.T[row][col + i] * sm.beta[col + i];
-            m = max(m, mag(t[i]));
+        for (int i = 0; i < 4; ++i) {
+            const float4 x = *reinterpret_cast<const float4 *>(&sm.T[row][col + 4 * i]);
+            const float4 y = *reinterpret_cast<const float4 *>(&sm.beta[col + 4 * i]);
+            t[i] = make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w);
+            m = max(max(max(m, mag(t[i].x)), max(mag(t[i].y), mag(t[i].z))), mag(t[i].w));
         }
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) sm.top[3][b] = m;
         __syncthreads();  // also: nobody reads L any more
         const float up_t = scale_up(top_of(sm.top[3]));
+        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            uint32_t hi, lo;
-            split2(t[i] * up_t, t[i + 1] * up_t, hi, lo);
-            *reinterpret_cast<uint32_t *>(&sm.l.t.hi[row][col + i]) = hi;
-            *reinterpret_cast<uint32_t *>(&sm.l.t.lo[row][col + i]) = lo;
+        for (int i = 0; i < 4; ++i) {
+            split2(make_float2(t[i].x * up_t, t[i].y * up_t), hi[2 * i], lo[2 * i]);
+            split2(make_float2(t[i].z * up_t, t[i].w * up_t), hi[2 * i + 1], lo[2 * i + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            *reinterpret_cast<uint4 *>(&sm.l.t.hi[row][col + 2 * i]) = make_uint4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
+            *reinterpret_cast<uint4 *>(&sm.l.t.lo[row][col + 2 * i]) = make_uint4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
         }
     }
     __syncthreads();
     const float down_t = scale_down(top_of(sm.top[3]));
     constexpr int NT = D / 64;  // 8-column tiles of a warp
     const int ar = lane % 16, ak = lane / 16 * 8;
-    float acc[4][NT][4] = {};
+    float acc[4][NT][4] = {}, acu[4][NT][4] = {};
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
-        uint32_t bh[NT][2], bl[NT][2];
+        uint32_t bh[NT][2], bl[NT][2], bv[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             ldsm2t(bh[x], smem_u32(&sm.x.kg.k_hi[ks * 16 + ar][(b * NT + x) * 8]));
             ldsm2t(bl[x], smem_u32(&sm.x.kg.k_lo[ks * 16 + ar][(b * NT + x) * 8]));
+            ldsm2t(bv[x], smem_u32(&sm.v[ks * 16 + ar][(b * NT + x) * 8]));
         }
 #pragma unroll
         for (int m = ks; m < 4; ++m) {
@@ -606,6 +726,8 @@ __global__ void __launch_bounds__(256, 2)
                 mma16(acc[m][x], ah, bh[x]);
                 mma16(acc[m][x], al, bh[x]);
                 mma16(acc[m][x], ah, bl[x]);
+                mma16(acu[m][x], ah, bv[x]);
+                mma16(acu[m][x], al, bv[x]);
             }
         }
     }
@@ -623,42 +745,27 @@ __global__ void __launch_bounds__(256, 2)
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) sm.top[0][b] = top;
     }
-    float acu[4][NT][4] = {};
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-        uint32_t bh[NT][2];
-#pragma unroll
-        for (int x = 0; x < NT; ++x) ldsm2t(bh[x], smem_u32(&sm.v[ks * 16 + ar][(b * NT + x) * 8]));
-#pragma unroll
-        for (int m = ks; m < 4; ++m) {
-            uint32_t ah[4], al[4];
-            ldsm4(ah, smem_u32(&sm.l.t.hi[m * 16 + ar][ks * 16 + ak]));
-            ldsm4(al, smem_u32(&sm.l.t.lo[m * 16 + ar][ks * 16 + ak]));
-#pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                mma16(acu[m][x], ah, bh[x]);
-                mma16(acu[m][x], al, bh[x]);
-            }
-        }
-    }
     __syncthreads();
     const float top_w = top_of(sm.top[0]);
-    const float up_w = scale_up(top_w);
+    const float up_w = scale_up(top_w), down_u = down_t * down_v;
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int x = 0; x < NT; ++x) {
+        const int col = (b * NT + x) * 8 + cc;  // rows g + 8 i: the swizzle's row is g
+        char *wo = out + Slot<D>::qw + (col >> 6) * Slot<D>::kBlock + (64 + g) * 128 + (((col >> 3 & 7) ^ g) << 4) + cc * 2;
+        char *uo = out + Slot<D>::u + (g * D + col) * 4;
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
+        for (int m = 0; m < 4; ++m)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-                const int row = m * 16 + g + e * 4, col = (b * NT + x) * 8 + cc;
                 uint32_t hi, lo;
-                split2(acc[m][x][e] * up_w, acc[m][x][e + 1] * up_w, hi, lo);
-                const int at = image_at(row, col, 64);
-                *reinterpret_cast<uint32_t *>(out + Slot<D>::w_hi + at) = hi;
-                *reinterpret_cast<uint32_t *>(out + Slot<D>::w_lo + at) = lo;
-                *reinterpret_cast<float2 *>(out + Slot<D>::u + (row * D + col) * 4) =
-                    make_float2(acu[m][x][e] * down_t * down_v, acu[m][x][e + 1] * down_t * down_v);
+                split2(mul2(make_float2(acc[m][x][e], acc[m][x][e + 1]), make_float2(up_w, up_w)), hi, lo);
+                const int row = m * 16 + e * 4;
+                *reinterpret_cast<uint32_t *>(wo + row * 128) = hi;
+                *reinterpret_cast<uint32_t *>(wo + row * 128 + 64 * 128) = lo;
+                *reinterpret_cast<float2 *>(uo + row * D * 4) =
+                    mul2(make_float2(acu[m][x][e], acu[m][x][e + 1]), make_float2(down_u, down_u));
             }
+    }
     if (threadIdx.x == 0) {
         float *f = reinterpret_cast<float *>(out + Slot<D>::scales);
         f[0] = scale_down(top_w);
@@ -698,11 +805,12 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     *abort = 1;
     return false;
 }
-// The 256 threads of the compute warps meet; true if any of them brings true.
+// kCount threads meet at barrier kId; true if any of them brings true.
+template <int kId, int kCount>
 __device__ __forceinline__ bool meet_any(bool bad) {
     uint32_t r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 256, p;\n"
-                 "selp.u32 %0, 1, 0, q;\n}" : "=r"(r) : "r"((uint32_t)bad) : "memory");
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, %2, %3, p;\n"
+                 "selp.u32 %0, 1, 0, q;\n}" : "=r"(r) : "r"((uint32_t)bad), "n"(kId), "n"(kCount) : "memory");
     return r != 0;
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -727,13 +835,16 @@ __device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t at) {
                    "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(at));
 }
-__device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t (&r)[16]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-                 ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-                   "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+__device__ __forceinline__ void tc_ld8(uint32_t (&r)[8], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at));
+}
+__device__ __forceinline__ void tc_st8(uint32_t at, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
-
 // Descriptor of an operand image in shared memory: K-major, 128-byte swizzle,
 // 8-row groups 1024 bytes apart (bit 46: the descriptor's version).
 __device__ __forceinline__ uint64_t operand_desc(uint32_t at) {
@@ -754,353 +865,541 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint3
 // ------------------------------------------------------------------ walk
 
 // What a walk does: write outputs and final states, or the two summaries of a
-// segment (its end state from zero or from the cached state, and from the identity).
+// segment: its end state from zero or from the cached state (B), and from the
+// identity (M), as two walks that share the chunk's operands and fill each
+// other's waits.
 enum { kWalkOut = 0, kWalkSummary = 1 };
+
+constexpr int kComputeWarps = 16, kCompute = kComputeWarps * 32;
+template <int kMode>
+constexpr int kWalkThreads = kCompute + (kMode == kWalkOut ? 256 : 128);
+
+// Registers of a thread: what a block is launched with, and how its roles share
+// that out (setmaxnreg): the sums over the threads are equal.
+template <int kMode>
+struct Regs {
+    static constexpr bool kOut = kMode == kWalkOut;
+    static constexpr int launch = kOut ? 80 : 96, compute = kOut ? 88 : 104, output = 72, rest = kOut ? 56 : 64;
+    static_assert(launch * kWalkThreads<kMode> == compute * kCompute + (kOut ? output * 128 : 0) + rest * 128, "");
+};
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// One item of a walk: a segment of a sequence, and one head.
+struct Item {
+    int64_t begin, stop;    // token rows
+    const char *slots;      // its first chunk's slot
+    const float *from;      // state to start from (NULL: zero)
+    float *to;              // where the final state goes (NULL: nowhere)
+    float *to_m;            // the same for the identity's walk (NULL: it is not walked)
+    int chunks;             // 0: no more items
+    int head;
+};
+
+enum {
+    kWFull = 0, kWEmpty = 2, kKFull = 4, kKEmpty = 6, kUFull = 8, kUEmpty = 10, kAFull = 12, kAEmpty = 13,
+    kSReady = 14, kPDone = 16, kVReady = 18, kDDone = 20, kODone = 22, kOFree = 24, kItemFull = 26,
+    kItemEmpty = 28, kBars = 30
+};
 
 template <int D, int kMode>
 struct WalkSmem {
-    static constexpr int kStages = 2;
     static constexpr bool kOut = kMode == kWalkOut;
-    static constexpr int kKStages = kOut ? 1 : 2;
-    alignas(1024) char w[kStages][2 * Slot<D>::kW];  // hi, lo
+    static constexpr int kStages = 2, kKStages = kOut ? 1 : 2;
+    static constexpr int kRows = kOut ? 192 : 128;         // rows of the image of (q and) W
+    static constexpr int kWBytes = kRows * D * 2;
+    static constexpr int kRow = D + 8;
+    alignas(1024) char w[kStages][kWBytes];
     char kk[kKStages][2 * Slot<D>::kW];
-    char q[kOut ? kStages : 1][kOut ? Slot<D>::kW : 1024];
     char a[kOut ? 8192 : 1024];
     float u[kStages][kChunk * D];
-    float meta[kStages][D + 16];  // G_63 and the scales of the chunk
-    float top[2][2][128];         // row maxima of the two halves: of S, of V'
-    float row_scale[2][2][128];   // unscaling of S and V' rows, for the outputs
-    uint64_t bars[24];
+    uint16_t o[kOut ? kChunk : 1][kRow];
+    alignas(16) float meta[kStages][D + 16];  // G_63 and the scales of the chunk
+    // Row maxima of the four column groups, of a walk's S and V' in turn: who writes the
+    // next has waited for a product that waited for everyone's reading of the last.
+    float top[kOut ? 1 : 2][4][128];
+    float row_scale[2][4][128];               // unscaling of S and V' rows, for the outputs, four chunks
+    Item item[2];
+    uint64_t bars[kBars];
     int abort;
     uint32_t tmem;
 };
 
-enum {
-    kWFull = 0, kWEmpty = 2, kKFull = 4, kKEmpty = 6, kQFull = 8, kQEmpty = 10, kUFull = 12, kUEmpty = 14,
-    kAFull = 16, kAEmpty = 17, kSReady = 18, kPDone = 19, kVReady = 20, kDDone = 21, kODone = 22, kOFree = 23
-};
-
-// TMEM columns (D = 128): hi and lo of S, P, o's two parts, hi and lo of V', the state's update.
-template <int D>
+// TMEM columns. Of a walk: S as halves (hi, then lo), overwritten by the state's
+// update D once P is done; P = W S^T in two parts (W hi and W lo), the second
+// then overwritten by V' as halves, the first by the second part of o. The
+// first part of o stands before P, so that one MMA writes [o | P | P2]; that
+// group alternates between two places, so that o may be read a chunk later.
+template <int D, int kMode>
 struct Cols {
-    static constexpr int s_hi = 0, s_lo = D / 2, p = D, o1 = D + 64, v_hi = D + 128, v_lo = D + 160,
-                         d = D + 192, o2 = 2 * D + 192;  // + 64 = 2 D + 256 <= 512
+    static constexpr int s = 0, d = 0, o1 = D, p = kMode == kWalkOut ? D + 64 : D, p2 = p + 64, v = p2, o2 = p;
+    static constexpr int walk = kMode == kWalkOut ? 0 : 256;  // columns from one walk to the next
+    static constexpr int turn = kMode == kWalkOut ? 192 : 0;  // from an even chunk's [o | P | P2] to an odd one's
 };
 
 struct WalkArgs {
     char *ws;
     float *summary;        // [segment slot][head][2][D][D]: B, M
-    float *first;          // [segment slot][head][D][D]: the state a later segment starts from
+    float *first;          // [segment slot][head][D][D]: the state a segment starts from
     int64_t seg_tokens;    // tokens of a segment (a multiple of 64)
+    int64_t items;
     int short_len;
-    int split;             // segments are searched for; 0: item = sequence
+    int split;             // whether a sequence can have more than one segment
 };
 
-constexpr int kWalkThreads = 448;  // 8 compute warps, 4 output warps, a tensor-core warp, a copy warp
-
-// Rows of `values` of one group scaled to halves: hi and lo packed pairs.
-template <int N>
-__device__ __forceinline__ float max_abs(const float (&f)[N]) {
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(f[i]));
-    return m;
+// The segment and head of item i; chunks = 0 where there is nothing to do.
+template <int D, int kMode>
+__device__ __forceinline__ Item load_item(const DeltaParams &p, const WalkArgs &w, int64_t i) {
+    Item it = {};
+    const int64_t at = i / p.heads;
+    it.head = i % p.heads;
+    int s;
+    int64_t seg = 0;
+    if (kMode == kWalkSummary) {
+        // Every segment but the last of a sequence holds exactly one multiple of seg_tokens.
+        const int64_t t = at * w.seg_tokens;
+        int lo = 0, hi = p.num_seqs - 1;
+        while (lo < hi) {  // the last sequence that starts at or before t
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.query_start_loc[mid] <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        s = lo;
+    } else {
+        s = w.split ? find_seq(p, at, w.seg_tokens, seg) : (int)at;
+    }
+    const Seq seq = load_seq(p, s);
+    const int64_t len = seq.end - seq.start;
+    if (kMode == kWalkSummary) {
+        if (at * w.seg_tokens < seq.start) return it;
+        seg = (at * w.seg_tokens - seq.start) / w.seg_tokens;
+    }
+    if (len <= w.short_len || seg < 0 || seg * w.seg_tokens >= len) return it;
+    const bool last = (seg + 1) * w.seg_tokens >= len;
+    if (kMode == kWalkSummary && last) return it;
+    it.begin = seq.start + seg * w.seg_tokens;
+    it.stop = last ? seq.end : it.begin + w.seg_tokens;
+    it.chunks = (int)((it.stop - it.begin + kChunk - 1) / kChunk);
+    it.slots = w.ws + kHeader +
+        ((seq.start / kChunk + s + seg * (w.seg_tokens / kChunk)) * p.heads + it.head) * slot_bytes(D);
+    const int64_t seg_at = (seq.start / w.seg_tokens + s + seg) * p.heads + it.head;
+    float *line = p.states + (seq.line < 0 ? 0 : seq.line) * p.ss[0] + it.head * p.ss[1];
+    if (kMode == kWalkOut) {
+        if (seg == 0 && last) it.from = seq.reads ? line : nullptr;
+        else it.from = w.first + seg_at * D * D;
+        it.to = last && seq.line >= 0 ? line : nullptr;
+    } else {
+        it.from = seg == 0 && seq.reads ? line : nullptr;
+        it.to = w.summary + seg_at * 2 * D * D;
+        it.to_m = seg > 0 ? it.to + D * D : nullptr;
+    }
+    return it;
 }
 
+// Blocks stay resident and take the next item from a counter in the workspace
+// (which block gets an item changes nothing in its result); the copy warp runs
+// ahead into the next item. Every role keeps a running chunk number n for
+// the rings' parities.
 template <typename T, int D, int kMode>
-__global__ void __launch_bounds__(kWalkThreads, 1)
+__global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
     delta_walk_kernel(const __grid_constant__ DeltaParams p, const __grid_constant__ WalkArgs w) {
     using Sm = WalkSmem<D, kMode>;
-    using Col = Cols<D>;
+    using Col = Cols<D, kMode>;
     constexpr bool kOut = kMode == kWalkOut;
-    constexpr int H = D / 2;  // state columns of a thread
+    constexpr int kWalks = kOut ? 1 : 2;
+    constexpr int CW = D / 4;  // state columns of a thread
+    constexpr int kOutWarps = kOut ? 4 : 0;
+    constexpr int kMmaWarp = kComputeWarps + kOutWarps, kCopyWarp = kMmaWarp + 1;  // and two that idle
     extern __shared__ __align__(1024) char raw_smem[];
     // The operand images start on 1024 bytes (the swizzle's period).
     Sm &sm = *reinterpret_cast<Sm *>(raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023));
-    dependency_wait();
-
-    // ---- the segment
-    const int which = kOut ? 0 : blockIdx.x % 2;  // summary: 0 the state's part (B), 1 the identity's (M)
-    const int64_t item = blockIdx.x / (kOut ? 1 : 2);
-    const int64_t seg_slot = item / p.heads;
-    const int h = item % p.heads;
-    int64_t seg = 0;
-    const int s = w.split ? find_seq(p, seg_slot, w.seg_tokens, seg) : (int)seg_slot;
-    const Seq seq = load_seq(p, s);
-    const int64_t len = seq.end - seq.start;
-    if (len <= w.short_len || seg < 0 || seg * w.seg_tokens >= len) return;
-    const bool last_seg = (seg + 1) * w.seg_tokens >= len;
-    // A sequence's last segment is never summarised, its first has no use for M.
-    if (!kOut && (last_seg || (which == 1 && seg == 0))) return;
-    const int64_t begin = seq.start + seg * w.seg_tokens;
-    const int64_t stop = last_seg ? seq.end : begin + w.seg_tokens;
-    const int chunks = (int)((stop - begin + kChunk - 1) / kChunk);
-    const char *slots = w.ws + kHeader +
-        ((seq.start / kChunk + s + seg * (w.seg_tokens / kChunk)) * p.heads + h) * slot_bytes(D);
-    const int64_t slot_step = (int64_t)p.heads * slot_bytes(D);
-
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t bars = smem_u32(sm.bars);
     volatile int *abort = &sm.abort;
     auto bar = [&](int i) { return bars + i * 8; };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 24; ++i) {
+        for (int i = 0; i < kBars; ++i) {
             int count = 1;
-            if (i == kSReady || i == kVReady) count = 8;
-            if (i == kUEmpty || i == kUEmpty + 1) count = kOut ? 12 : 8;
-            if (i == kOFree) count = 4;
+            if (i >= kSReady && i < kSReady + 2) count = kComputeWarps;
+            if (i >= kVReady && i < kVReady + 2) count = kComputeWarps;
+            if (i >= kUEmpty && i < kUEmpty + 2) count = kComputeWarps + kOutWarps;
+            if (i >= kItemEmpty) count = kComputeWarps + kOutWarps + 1;
+            if (i >= kOFree && i < kOFree + 2) count = 4;
             bar_init(bar(i), count);
         }
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    dependency_wait();
     tc_before();
     __syncthreads();
     tc_after();
     const uint32_t tmem = sm.tmem;
 
-    if (warp < 8) {
-        // ---- compute warps: row v of the state, columns [half * H, half * H + H)
-        const int half = warp / 4, v = warp % 4 * 32 + lane;
+    if (warp < kComputeWarps) {
+        more_registers<Regs<kMode>::compute>();
+        // ---- compute warps: row v of the state, CW columns; V' of 16 tokens
+        const int part = warp / 4, v = warp % 4 * 32 + lane;
         const uint32_t mine = tmem + ((uint32_t)(warp % 4 * 32) << 16);
         const bool row_in = v < D;
-        float S[H];
-#pragma unroll
-        for (int i = 0; i < H; ++i) S[i] = 0.0f;
-        if (row_in) {
-            const float *from = nullptr;
-            if (kOut && !(seg == 0 && last_seg)) from = w.first + ((seg_slot * p.heads + h) * D + v) * D;
-            else if (which == 0 && seg == 0 && seq.reads) from = p.states + seq.line * p.ss[0] + h * p.ss[1] + v * D;
-            if (from != nullptr) {
-#pragma unroll
-                for (int i = 0; i < H; i += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(from + half * H + i);
-                    S[i] = f.x, S[i + 1] = f.y, S[i + 2] = f.z, S[i + 3] = f.w;
-                }
-            } else if (which == 1) {
-#pragma unroll
-                for (int i = 0; i < H; ++i) S[i] = half * H + i == v ? 1.0f : 0.0f;
-            }
-        }
+        float2 S[kWalks][CW / 2];
         bool bad = false;
-        for (int c = 0; c < chunks; ++c) {
-            const uint32_t par = c & 1, ring = c >> 1 & 1;
-            // S as halves
-            sm.top[0][half][v] = max_abs(S);
-            if (meet_any(bad)) { bad = true; break; }
-            const float top_s = fmaxf(sm.top[0][0][v], sm.top[0][1][v]);
-            const float up_s = scale_up(top_s), down_s = scale_down(top_s);
+        uint32_t n = 0, n1 = 0;  // chunks so far, and those of the identity's walk
+        for (uint32_t k = 0;; ++k) {
+            bad = !bar_wait(bar(kItemFull + (k & 1)), k >> 1 & 1, abort);
+            if (meet_any<1, kCompute>(bad)) break;
+            const int chunks = sm.item[k & 1].chunks;
+            if (chunks == 0) break;
+            const float *from = sm.item[k & 1].from;
+            const int walks = !kOut && sm.item[k & 1].to_m != nullptr ? 2 : 1;
 #pragma unroll
-            for (int i = 0; i < H; i += 32) {
-                uint32_t hi[16], lo[16];
+            for (int i = 0; i < CW / 2; ++i) S[0][i] = make_float2(0.0f, 0.0f);
+            if (row_in && from != nullptr) {
+                from += v * D + part * CW;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) split2(S[i + 2 * j] * up_s, S[i + 2 * j + 1] * up_s, hi[j], lo[j]);
-                tc_st16(mine + Col::s_hi + (half * H + i) / 2, hi);
-                tc_st16(mine + Col::s_lo + (half * H + i) / 2, lo);
-            }
-            if (kOut && half == 0) sm.row_scale[0][par][v] = down_s;
-            tc_wait_st();
-            tc_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(kSReady));
-            // V' = U - W S^T: this thread's 32 tokens
-            bad = !bar_wait(bar(kUFull + par), ring, abort) || !bar_wait(bar(kPDone), par, abort);
-            tc_after();
-            const float *meta = sm.meta[par];
-            const float down_p = meta[D], down_k = meta[D + 1];
-            float V[32];
-            {
-                uint32_t r0[16], r1[16];
-                tc_ld16(r0, mine + Col::p + half * 32);
-                tc_ld16(r1, mine + Col::p + half * 32 + 16);
-                tc_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    V[j] = __uint_as_float(r0[j]) * down_p * down_s;
-                    V[16 + j] = __uint_as_float(r1[j]) * down_p * down_s;
+                for (int i = 0; i < CW; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(from + i);
+                    S[0][i / 2] = make_float2(f.x, f.y), S[0][i / 2 + 1] = make_float2(f.z, f.w);
                 }
             }
-            const bool uses_u = (kOut || which == 0) && row_in;
+            if constexpr (!kOut)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) V[j] = (uses_u ? sm.u[par][(half * 32 + j) * D + v] : 0.0f) - V[j];
-            sm.top[1][half][v] = max_abs(V);
-            if (kOut && c > 0) bad |= !bar_wait(bar(kODone), (c - 1) & 1, abort);  // V' of the last chunk is still read
-            if (meet_any(bad)) { bad = true; break; }
-            const float top_v = fmaxf(sm.top[1][0][v], sm.top[1][1][v]);
-            const float up_v = scale_up(top_v), down_v = scale_down(top_v);
-            {
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) split2(V[2 * j] * up_v, V[2 * j + 1] * up_v, hi[j], lo[j]);
-                tc_st16(mine + Col::v_hi + half * 16, hi);
-                tc_st16(mine + Col::v_lo + half * 16, lo);
-            }
-            if (kOut && half == 0) sm.row_scale[1][par][v] = down_v;
-            tc_wait_st();
-            tc_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(kVReady));
+                for (int i = 0; i < CW; i += 2)
+                    S[1][i / 2] = make_float2(part * CW + i == v ? 1.0f : 0.0f, part * CW + i + 1 == v ? 1.0f : 0.0f);
+            float down_s[kWalks], down_v[kWalks] = {};
             // S = S diag(G_63) + V'^T (k G_63 / G)
-            bad = !bar_wait(bar(kDDone), par, abort);
-            tc_after();
-#pragma unroll
-            for (int i = 0; i < H; i += 16) {
-                uint32_t r[16];
-                tc_ld16(r, mine + Col::d + half * H + i);
-                float4 gs[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) gs[j] = *reinterpret_cast<const float4 *>(meta + half * H + i + 4 * j);
-                tc_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    S[i + 4 * j] = fmaf(S[i + 4 * j], gs[j].x, __uint_as_float(r[4 * j]) * down_k * down_v);
-                    S[i + 4 * j + 1] = fmaf(S[i + 4 * j + 1], gs[j].y, __uint_as_float(r[4 * j + 1]) * down_k * down_v);
-                    S[i + 4 * j + 2] = fmaf(S[i + 4 * j + 2], gs[j].z, __uint_as_float(r[4 * j + 2]) * down_k * down_v);
-                    S[i + 4 * j + 3] = fmaf(S[i + 4 * j + 3], gs[j].w, __uint_as_float(r[4 * j + 3]) * down_k * down_v);
-                }
-            }
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(kUEmpty + par));  // U and the chunk's scales are read
-        }
-        bad = meet_any(bad);
-        if (!bad && row_in) {
-            float *to = nullptr;
-            if (!kOut) to = w.summary + (((seg_slot * p.heads + h) * 2 + which) * D + v) * D;
-            else if (last_seg && seq.line >= 0) to = p.states + seq.line * p.ss[0] + h * p.ss[1] + v * D;
-            if (to != nullptr)
-#pragma unroll
-                for (int i = 0; i < H; i += 4)
-                    *reinterpret_cast<float4 *>(to + half * H + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
-        }
-    } else if (warp < 12) {
-        // ---- output warps: row v, all tokens of the chunk
-        if constexpr (kOut) {
-            const int v = warp % 4 * 32 + lane;
-            const uint32_t mine = tmem + ((uint32_t)(warp % 4 * 32) << 16);
-            T *out = static_cast<T *>(p.out) + h * p.os[1] + v;
-            for (int c = 0; c < chunks; ++c) {
-                const uint32_t par = c & 1, ring = c >> 1 & 1;
-                // The copy of the chunk's scales is visible only to who has waited for it.
-                if (!bar_wait(bar(kUFull + par), ring, abort) || !bar_wait(bar(kODone), par, abort)) break;
+            auto update = [&](int x) {  // of the last chunk counted
+                bad |= !bar_wait(bar(kDDone + x), ((x ? n1 : n) - 1) & 1, abort);
                 tc_after();
-                const float *meta = sm.meta[par];
-                const float f1 = meta[D + 2], f2 = meta[D + 3], f3 = meta[D + 4];
-                const float ds = sm.row_scale[0][par][v], dv = sm.row_scale[1][par][v];
-                float o[64];
+                const float *meta = sm.meta[(n - 1) & 1];
+                const float down_k = meta[D + 1], dv = down_v[x];
 #pragma unroll
-                for (int i = 0; i < 64; i += 16) {
-                    uint32_t r[16], x[16];
-                    tc_ld16(r, mine + Col::o1 + i);
-                    tc_ld16(x, mine + Col::o2 + i);
+                for (int i = 0; i < CW; i += 16) {
+                    uint32_t r[16];
+                    tc_ld16(r, mine + x * Col::walk + Col::d + part * CW + i);
                     tc_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        o[i + j] = p.scale * (__uint_as_float(r[j]) * f1 * ds + __uint_as_float(x[j]) * f2 * f3 * dv);
-                }
-                tc_before();
-                __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(bar(kOFree));
-                    bar_arrive(bar(kUEmpty + par));
-                }
-                const int64_t t0 = begin + (int64_t)c * kChunk;
-                const int n = (int)min((int64_t)kChunk, stop - t0);
-                if (v < D) {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        if (j < n) out[(t0 + j) * p.os[0]] = from_f<T>(o[j]);
-                }
-            }
-        }
-    } else if (warp == 12) {
-        // ---- tensor-core warp
-        if (lane == 0) {
-            constexpr uint32_t id_n64 = instr_desc(64), id_d = instr_desc(D);
-            for (int c = 0; c < chunks; ++c) {
-                const uint32_t par = c & 1, ring = c >> 1 & 1;
-                const uint32_t kst = Sm::kKStages == 2 ? par : 0, kring = Sm::kKStages == 2 ? ring : par;
-                if (!bar_wait(bar(kWFull + par), ring, abort) || !bar_wait(bar(kSReady), par, abort)) break;
-                tc_after();
-                {
-                    const uint32_t hi = smem_u32(sm.w[par]), lo = hi + Slot<D>::kW;
-#pragma unroll
-                    for (int i = 0; i < 3 * (D / 16); ++i) {
-                        const int k = i % (D / 16), term = i / (D / 16);  // hi hi, hi lo, lo hi
-                        const uint32_t b = (term == 1 ? lo : hi) + k / 4 * 8192 + k % 4 * 32;
-                        tc_mma(tmem + Col::p, tmem + (term == 2 ? Col::s_lo : Col::s_hi) + k * 8, operand_desc(b),
-                               id_n64, i != 0);
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 gs = *reinterpret_cast<const float4 *>(meta + part * CW + i + j);
+                        const float2 dk2 = make_float2(down_k, down_k), dv2 = make_float2(dv, dv);
+                        const float2 x0 = mul2(mul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), dk2), dv2);
+                        const float2 x1 = mul2(mul2(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), dk2), dv2);
+                        S[x][(i + j) / 2] = fma2(S[x][(i + j) / 2], make_float2(gs.x, gs.y), x0);
+                        S[x][(i + j) / 2 + 1] = fma2(S[x][(i + j) / 2 + 1], make_float2(gs.z, gs.w), x1);
                     }
                 }
-                tc_commit(bar(kPDone));
-                tc_commit(bar(kWEmpty + par));
-                if (kOut) {
-                    if (!bar_wait(bar(kQFull + par), ring, abort)) break;
-                    if (c > 0 && !bar_wait(bar(kOFree), (c - 1) & 1, abort)) break;
+            };
+            for (int c = 0; c < chunks; ++c, ++n, n1 += walks - 1) {
+                const uint32_t par = n & 1, ring = n >> 1 & 1;
+#pragma unroll
+                for (int x = 0; x < kWalks; ++x) {
+                    if (x >= walks) break;
+                    if (c > 0) update(x);
+                    // S as halves
+                    float top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < CW / 2; ++i) top = fmaxf(top, fmaxf(fabsf(S[x][i].x), fabsf(S[x][i].y)));
+                    sm.top[x][part][v] = top;
+                    tc_before();  // S's columns are D's, which others read
+                    if (meet_any<1, kCompute>(bad)) { bad = true; break; }
                     tc_after();
-                    const uint32_t q = smem_u32(sm.q[par]);
+                    top = fmaxf(fmaxf(sm.top[x][0][v], sm.top[x][1][v]), fmaxf(sm.top[x][2][v], sm.top[x][3][v]));
+                    const float up = scale_up(top);
+                    down_s[x] = scale_down(top);
+                    uint32_t hi[CW / 2], lo[CW / 2];
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc_mma(tmem + Col::o1, tmem + Col::s_hi + k * 8, operand_desc(q + k / 4 * 8192 + k % 4 * 32),
-                               id_n64, k != 0);
-                    tc_commit(bar(kQEmpty + par));
-                }
-                if (!bar_wait(bar(kKFull + kst), kring, abort) || !bar_wait(bar(kVReady), par, abort)) break;
-                tc_after();
-                {
-                    const uint32_t hi = smem_u32(sm.kk[kst]), lo = hi + Slot<D>::kW;
+                    for (int i = 0; i < CW / 2; ++i) split2(mul2(S[x][i], make_float2(up, up)), hi[i], lo[i]);
+                    const uint32_t at = mine + x * Col::walk + Col::s + part * (CW / 2);
 #pragma unroll
-                    for (int i = 0; i < 12; ++i) {
-                        const int k = i % 4, term = i / 4;
-                        tc_mma(tmem + Col::d, tmem + (term == 2 ? Col::v_lo : Col::v_hi) + k * 8,
-                               operand_desc((term == 1 ? lo : hi) + k * 32), id_d, i != 0);
+                    for (int i = 0; i < CW / 2; i += 8) {
+                        tc_st8(at + i, hi + i);
+                        tc_st8(at + D / 2 + i, lo + i);
                     }
+                    if (kOut && part == 0) sm.row_scale[0][n & 3][v] = down_s[x];
+                    tc_wait_st();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar(kSReady + x));
                 }
-                tc_commit(bar(kDDone));
-                tc_commit(bar(kKEmpty + kst));
-                if (kOut) {
-                    if (!bar_wait(bar(kAFull), par, abort)) break;
-                    const uint32_t a = smem_u32(sm.a);
+                if (bad) break;
+                if (c > 0) {  // every update of the last chunk is done: U and its scales are read
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar(kUEmpty + (par ^ 1)));
+                }
+                bad = !bar_wait(bar(kUFull + par), ring, abort);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma(tmem + Col::o2, tmem + Col::v_hi + k * 8, operand_desc(a + k * 32), id_n64, k != 0);
-                    tc_commit(bar(kODone));
-                    tc_commit(bar(kAEmpty));
+                for (int x = 0; x < kWalks; ++x) {
+                    if (x >= walks) break;
+                    // V' = U - W S^T
+                    float2 V[8];
+                    if (x == 0 && row_in) {
+                        const float *u = &sm.u[par][part * 16 * D + v];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) V[j] = make_float2(u[2 * j * D], u[(2 * j + 1) * D]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) V[j] = make_float2(0.0f, 0.0f);
+                    }
+                    bad |= !bar_wait(bar(kPDone + x), (x ? n1 : n) & 1, abort);
+                    tc_after();
+                    {
+                        const float down_w = sm.meta[par][D];
+                        const float2 dw = make_float2(down_w, down_w), ds = make_float2(-down_s[x], -down_s[x]);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 8) {
+                            uint32_t r0[8], r1[8];
+                            tc_ld8(r0, mine + x * Col::walk + par * Col::turn + Col::p + part * 16 + j);
+                            tc_ld8(r1, mine + x * Col::walk + par * Col::turn + Col::p2 + part * 16 + j);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                const float2 f = __fadd2_rn(make_float2(__uint_as_float(r0[i]), __uint_as_float(r0[i + 1])),
+                                                            make_float2(__uint_as_float(r1[i]), __uint_as_float(r1[i + 1])));
+                                V[(i + j) / 2] = fma2(mul2(f, dw), ds, V[(i + j) / 2]);
+                            }
+                        }
+                    }
+                    float top = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(V[j].x), fabsf(V[j].y)));
+                    sm.top[x][part][v] = top;
+                    tc_before();
+                    if (meet_any<1, kCompute>(bad)) { bad = true; break; }
+                    tc_after();
+                    top = fmaxf(fmaxf(sm.top[x][0][v], sm.top[x][1][v]), fmaxf(sm.top[x][2][v], sm.top[x][3][v]));
+                    const float up = scale_up(top);
+                    down_v[x] = scale_down(top);
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) split2(mul2(V[j], make_float2(up, up)), hi[j], lo[j]);
+                    tc_st8(mine + x * Col::walk + par * Col::turn + Col::v + part * 8, hi);
+                    tc_st8(mine + x * Col::walk + par * Col::turn + Col::v + 32 + part * 8, lo);
+                    if (kOut && part == 0) sm.row_scale[1][n & 3][v] = down_v[x];
+                    tc_wait_st();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar(kVReady + x));
+                }
+                if (bad) break;
+            }
+            if (!bad)
+#pragma unroll
+                for (int x = 0; x < kWalks; ++x)
+                    if (x < walks) update(x);
+            tc_before();
+            // D's columns are S's: nobody writes the next item's S before all have read D.
+            if (meet_any<1, kCompute>(bad)) break;
+            tc_after();
+            if (lane == 0) bar_arrive(bar(kUEmpty + ((n - 1) & 1)));
+            if (row_in)
+#pragma unroll
+                for (int x = 0; x < kWalks; ++x) {
+                    float *dst = x == 0 ? sm.item[k & 1].to : sm.item[k & 1].to_m;
+                    if (dst == nullptr) continue;
+                    dst += v * D + part * CW;
+#pragma unroll
+                    for (int i = 0; i < CW; i += 4)
+                        *reinterpret_cast<float4 *>(dst + i) =
+                            make_float4(S[x][i / 2].x, S[x][i / 2].y, S[x][i / 2 + 1].x, S[x][i / 2 + 1].y);
+                }
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(kItemEmpty + (k & 1)));
+        }
+    } else if (kOut && warp < kMmaWarp) {
+        // ---- output warps: row v, all tokens of the chunk
+        if constexpr (kOut) {
+            fewer_registers<Regs<kMode>::output>();
+            const int v = warp % 4 * 32 + lane, tid = threadIdx.x - kCompute;
+            const uint32_t mine = tmem + ((uint32_t)(warp % 4 * 32) << 16);
+            uint32_t n = 0;
+            bool bad = false;
+            for (uint32_t k = 0; !bad; ++k) {
+                bad = !bar_wait(bar(kItemFull + (k & 1)), k >> 1 & 1, abort);
+                if (meet_any<2, 128>(bad)) break;
+                const int chunks = sm.item[k & 1].chunks;
+                const int64_t begin = sm.item[k & 1].begin, stop = sm.item[k & 1].stop;
+                T *out = static_cast<T *>(p.out) + sm.item[k & 1].head * p.os[1];
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(kItemEmpty + (k & 1)));
+                if (chunks == 0) break;
+                for (int c = 0; c < chunks; ++c, ++n) {
+                    const uint32_t par = n & 1, ring = n >> 1 & 1;
+                    // The copy of the chunk's scales is visible only to who has waited for it.
+                    bad = !bar_wait(bar(kUFull + par), ring, abort) || !bar_wait(bar(kODone + par), ring, abort);
+                    if (meet_any<2, 128>(bad)) { bad = true; break; }  // also: sm.o is free
+                    tc_after();
+                    const float *meta = sm.meta[par];
+                    const float f1 = meta[D + 2] * p.scale, f2 = meta[D + 3] * p.scale, f3 = meta[D + 4];
+                    const float ds = sm.row_scale[0][n & 3][v], dv = sm.row_scale[1][n & 3][v];
+#pragma unroll
+                    for (int i = 0; i < 64; i += 16) {
+                        uint32_t r[16], x[16];
+                        tc_ld16(r, mine + par * Col::turn + Col::o1 + i);
+                        tc_ld16(x, mine + par * Col::turn + Col::o2 + i);
+                        tc_wait_ld();
+                        if (v < D)
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                reinterpret_cast<T *>(sm.o[i + j])[v] =
+                                    from_f<T>(__uint_as_float(r[j]) * f1 * ds + __uint_as_float(x[j]) * f2 * f3 * dv);
+                    }
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        bar_arrive(bar(kOFree + par));
+                        bar_arrive(bar(kUEmpty + par));
+                    }
+                    asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
+                    const int64_t t0 = begin + (int64_t)c * kChunk;
+                    const int rows = (int)min((int64_t)kChunk, stop - t0);
+                    constexpr int kPieces = D / 8;  // 16-byte pieces of a row
+#pragma unroll
+                    for (int i = 0; i < kChunk; i += 128 / kPieces) {
+                        const int row = i + tid / kPieces, at = tid % kPieces * 8;
+                        if (row < rows)
+                            *reinterpret_cast<uint4 *>(out + (t0 + row) * p.os[0] + at) =
+                                *reinterpret_cast<const uint4 *>(&sm.o[row][at]);
+                    }
                 }
             }
         }
-    } else if (lane == 0) {
-        // ---- copy warp
-        for (int c = 0; c < chunks; ++c) {
-            const uint32_t par = c & 1, ring = c >> 1 & 1;
-            const uint32_t kst = Sm::kKStages == 2 ? par : 0, kring = Sm::kKStages == 2 ? ring : par;
-            const bool k_reused = Sm::kKStages == 2 ? c >= 2 : c >= 1;
-            const char *from = slots + c * slot_step;
-            if (c >= 2 && !bar_wait(bar(kWEmpty + par), ring ^ 1, abort)) break;
-            bar_expect(bar(kWFull + par), 2 * Slot<D>::kW);
-            bulk_load(smem_u32(sm.w[par]), from + Slot<D>::w_hi, 2 * Slot<D>::kW, bar(kWFull + par));
-            if (c >= 2 && !bar_wait(bar(kUEmpty + par), ring ^ 1, abort)) break;
-            bar_expect(bar(kUFull + par), kChunk * D * 4 + D * 4 + 64);
-            bulk_load(smem_u32(sm.u[par]), from + Slot<D>::u, kChunk * D * 4, bar(kUFull + par));
-            bulk_load(smem_u32(sm.meta[par]), from + Slot<D>::decay, D * 4 + 64, bar(kUFull + par));
-            if (kOut) {
-                if (c >= 2 && !bar_wait(bar(kQEmpty + par), ring ^ 1, abort)) break;
-                bar_expect(bar(kQFull + par), Slot<D>::kW);
-                bulk_load(smem_u32(sm.q[par]), from + Slot<D>::q, Slot<D>::kW, bar(kQFull + par));
+    } else {
+        fewer_registers<Regs<kMode>::rest>();
+        if (warp == kMmaWarp && lane == 0) {
+            // ---- the thread that issues to the tensor core
+            constexpr int kBlock = Sm::kRows * 128;  // an image's column block of 64
+            constexpr int kQ = kOut ? 64 : 0;        // rows before W
+            uint32_t n = 0, n1 = 0;
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                if (!bar_wait(bar(kItemFull + (k & 1)), k >> 1 & 1, abort)) break;
+                const int chunks = sm.item[k & 1].chunks;
+                const int walks = !kOut && sm.item[k & 1].to_m != nullptr ? 2 : 1;
+                bar_arrive(bar(kItemEmpty + (k & 1)));
+                if (chunks == 0) break;
+                for (int c = 0; c < chunks && ok; ++c, ++n, n1 += walks - 1) {
+                    const uint32_t par = n & 1, ring = n >> 1 & 1;
+                    const uint32_t kst = Sm::kKStages == 2 ? par : 0, kring = Sm::kKStages == 2 ? ring : par;
+                    ok = bar_wait(bar(kWFull + par), ring, abort);
+                    if (kOut && n > 1) ok = ok && bar_wait(bar(kOFree + par), ring ^ 1, abort);
+                    const uint32_t wi = smem_u32(sm.w[par]);
+#pragma unroll
+                    for (int x = 0; x < kWalks; ++x) {
+                        if (x >= walks) break;
+                        ok = ok && bar_wait(bar(kSReady + x), (x ? n1 : n) & 1, abort);
+                        if (!ok) break;
+                        tc_after();
+                        const uint32_t base = tmem + x * Col::walk, acc = base + par * Col::turn;
+                        // S hi [q | W hi | W lo]^T, then S lo [q | W hi]^T
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i)
+                            tc_mma(acc + (kOut ? Col::o1 : Col::p), base + Col::s + i * 8,
+                                   operand_desc(wi + i / 4 * kBlock + i % 4 * 32), instr_desc(kQ + 128), i != 0);
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i)
+                            tc_mma(acc + (kOut ? Col::o1 : Col::p), base + Col::s + D / 2 + i * 8,
+                                   operand_desc(wi + i / 4 * kBlock + i % 4 * 32), instr_desc(kQ + 64), true);
+                        tc_commit(bar(kPDone + x));
+                    }
+                    if (!ok) break;
+                    tc_commit(bar(kWEmpty + par));
+                    ok = bar_wait(bar(kKFull + kst), kring, abort);
+                    const uint32_t ki = smem_u32(sm.kk[kst]);
+#pragma unroll
+                    for (int x = 0; x < kWalks; ++x) {
+                        if (x >= walks) break;
+                        ok = ok && bar_wait(bar(kVReady + x), (x ? n1 : n) & 1, abort);
+                        if (!ok) break;
+                        tc_after();
+                        const uint32_t base = tmem + x * Col::walk, acc = base + par * Col::turn;
+#pragma unroll
+                        for (int i = 0; i < 12; ++i) {  // hi hi, hi lo, lo hi
+                            const int st = i % 4, term = i / 4;
+                            tc_mma(base + Col::d, acc + Col::v + (term == 2 ? 32 : 0) + st * 8,
+                                   operand_desc(ki + (term == 1 ? Slot<D>::kW : 0) + st * 32), instr_desc(D), i != 0);
+                        }
+                        tc_commit(bar(kDDone + x));
+                    }
+                    if (!ok) break;
+                    tc_commit(bar(kKEmpty + kst));
+                    if (kOut) {
+                        ok = bar_wait(bar(kAFull), par, abort);
+                        if (!ok) break;
+                        const uint32_t ai = smem_u32(sm.a), acc = tmem + par * Col::turn;
+                        constexpr int kTerms = !std::is_same<T, __nv_bfloat16>::value ? 8 : 4;
+#pragma unroll
+                        for (int i = 0; i < kTerms; ++i)  // V' hi, and for an fp16 result V' lo
+                            tc_mma(acc + Col::o2, acc + Col::v + (i / 4) * 32 + i % 4 * 8,
+                                   operand_desc(ai + i % 4 * 32), instr_desc(64), i != 0);
+                        tc_commit(bar(kODone + par));
+                        tc_commit(bar(kAEmpty));
+                    }
+                }
             }
-            if (k_reused && !bar_wait(bar(kKEmpty + kst), kring ^ 1, abort)) break;
-            bar_expect(bar(kKFull + kst), 2 * Slot<D>::kW);
-            bulk_load(smem_u32(sm.kk[kst]), from + Slot<D>::k_hi, 2 * Slot<D>::kW, bar(kKFull + kst));
-            if (kOut) {
-                if (c >= 1 && !bar_wait(bar(kAEmpty), par ^ 1, abort)) break;
-                bar_expect(bar(kAFull), kChunk * kChunk * 2);
-                bulk_load(smem_u32(sm.a), from + Slot<D>::a, kChunk * kChunk * 2, bar(kAFull));
+        }
+        if (warp == kCopyWarp && lane == 0) {
+            // ---- the thread that takes items and copies operands
+        const int64_t step = (int64_t)p.heads * slot_bytes(D);
+        uint32_t n = 0, k = 0;
+        bool ok = true;
+        int *counter = reinterpret_cast<int *>(w.ws) + (kOut ? 2 : 1);
+        int64_t next = blockIdx.x;
+        while (ok) {
+            const int64_t i = next;
+            if (i < w.items) next = gridDim.x + (int64_t)atomicAdd(counter, 1);
+            Item it = {};
+            if (i < w.items) {
+                it = load_item<D, kMode>(p, w, i);
+                if (it.chunks == 0) continue;
             }
+            if (k >= 2) ok = bar_wait(bar(kItemEmpty + (k & 1)), (k >> 1 & 1) ^ 1, abort);
+            if (!ok) break;
+            sm.item[k & 1] = it;
+            bar_arrive(bar(kItemFull + (k & 1)));
+            ++k;
+            if (it.chunks == 0) break;
+            if (it.from != nullptr)  // the next item's state, while the present one is walked
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(it.from), "r"(D * D * 4) : "memory");
+            for (int c = 0; c < it.chunks; ++c, ++n) {
+                const uint32_t par = n & 1, ring = n >> 1 & 1;
+                const uint32_t kst = Sm::kKStages == 2 ? par : 0, kring = Sm::kKStages == 2 ? ring : par;
+                const char *from = it.slots + c * step;
+                if (n >= 2) ok = bar_wait(bar(kWEmpty + par), ring ^ 1, abort);
+                if (!ok) break;
+                bar_expect(bar(kWFull + par), Sm::kWBytes);
+                if (kOut) {
+                    bulk_load(smem_u32(sm.w[par]), from + Slot<D>::qw, Sm::kWBytes, bar(kWFull + par));
+                } else {
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)
+                        bulk_load(smem_u32(sm.w[par]) + x * 16384, from + Slot<D>::qw + x * Slot<D>::kBlock + 8192,
+                                  16384, bar(kWFull + par));
+                }
+                if (n >= 2) ok = bar_wait(bar(kUEmpty + par), ring ^ 1, abort);
+                if (!ok) break;
+                bar_expect(bar(kUFull + par), kChunk * D * 4 + D * 4 + 64);
+                bulk_load(smem_u32(sm.u[par]), from + Slot<D>::u, kChunk * D * 4, bar(kUFull + par));
+                bulk_load(smem_u32(sm.meta[par]), from + Slot<D>::decay, D * 4 + 64, bar(kUFull + par));
+                if (Sm::kKStages == 2 ? n >= 2 : n >= 1) ok = bar_wait(bar(kKEmpty + kst), kring ^ 1, abort);
+                if (!ok) break;
+                bar_expect(bar(kKFull + kst), 2 * Slot<D>::kW);
+                bulk_load(smem_u32(sm.kk[kst]), from + Slot<D>::k_hi, 2 * Slot<D>::kW, bar(kKFull + kst));
+                if (kOut) {
+                    if (n >= 1) ok = bar_wait(bar(kAEmpty), par ^ 1, abort);
+                    if (!ok) break;
+                    bar_expect(bar(kAFull), kChunk * kChunk * 2);
+                    bulk_load(smem_u32(sm.a), from + Slot<D>::a, kChunk * kChunk * 2, bar(kAFull));
+                }
+            }
+        }
         }
     }
     tc_before();
@@ -1116,59 +1415,114 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         __syncthreads();
     }
     __syncwarp();
-    if (warp == 12)
+    if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // ------------------------------------------------------------------ join
 
-// first[0] = the cached state (the walk of the last segment overwrites it),
-// first[seg + 1] = (seg ? first[seg] M[seg] : 0) + B[seg], segment by segment:
-// one block per (sequence, head, kJoinRows rows of the state), a column per thread.
-constexpr int kJoinRows = 8;
+// For each sequence of several segments: first[0] = the cached state (the walk
+// of the last segment overwrites it), first[seg + 1] = (seg ? first[seg] M[seg]
+// : 0) + B[seg], segment by segment. A block takes kJoinRows rows of one
+// head's state; M comes by bulk copies, one segment ahead.
+constexpr int kJoinRows = 16, kJoinThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(D) delta_join_kernel(const __grid_constant__ DeltaParams p, const __grid_constant__ WalkArgs w) {
-    __shared__ float row[kJoinRows][D];
+struct JoinSmem {
+    float m[2][D * D];
+    float row[2][D][kJoinRows];
+    uint64_t full[2];
+    int abort;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_constant__ DeltaParams p,
+                                                                 const __grid_constant__ WalkArgs w) {
+    constexpr int R = kJoinRows * D / kJoinThreads;  // rows of a thread
+    extern __shared__ __align__(1024) char raw_smem[];
+    JoinSmem<D> &sm = *reinterpret_cast<JoinSmem<D> *>(raw_smem);
     dependency_wait();
-    const int s = blockIdx.x / p.heads, h = blockIdx.x % p.heads;
-    const int r0 = blockIdx.y * kJoinRows, k = threadIdx.x;
-    const Seq seq = load_seq(p, s);
+    // The sequence that holds token (multiple of seg_tokens) number blockIdx.x, if that is
+    // the first multiple in it: every sequence of several segments holds one.
+    const int64_t t = (int64_t)blockIdx.x * w.seg_tokens;
+    const int h = blockIdx.y;
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.query_start_loc[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    const Seq seq = load_seq(p, lo);
     const int64_t len = seq.end - seq.start;
-    if (len <= w.short_len || len <= w.seg_tokens) return;
+    if (t < seq.start || t - seq.start >= w.seg_tokens || len <= w.short_len || len <= w.seg_tokens) return;
     const int segs = (int)((len + w.seg_tokens - 1) / w.seg_tokens);
-    const int64_t base = seq.start / w.seg_tokens + s;
-    float S[kJoinRows];
+    const int64_t base = seq.start / w.seg_tokens + lo;
+    const int k = threadIdx.x % D, r0 = threadIdx.x / D * R, row0 = blockIdx.z * kJoinRows + r0;
+    auto at = [&](int seg) { return (base + seg) * p.heads + h; };
+    volatile int *abort = &sm.abort;
+    if (threadIdx.x == 0) {
+        sm.abort = 0;
+        bar_init(smem_u32(&sm.full[0]), 1);
+        bar_init(smem_u32(&sm.full[1]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
+    auto fetch = [&](int seg) {  // M of a segment (1 .. segs - 2)
+        const uint32_t bar = smem_u32(&sm.full[seg & 1]);
+        bar_expect(bar, D * D * 4);
+        bulk_load(smem_u32(sm.m[seg & 1]), w.summary + (at(seg) * 2 + 1) * D * D, D * D * 4, bar);
+    };
+    if (threadIdx.x == 0 && segs > 2) fetch(1);
+    if (threadIdx.x == 0 && segs > 3) fetch(2);
     {
         const float *from = p.states + (seq.reads ? seq.line : 0) * p.ss[0] + h * p.ss[1];
-        float *to = w.first + (base * p.heads + h) * D * D;
+        float *to = w.first + at(0) * D * D;
 #pragma unroll
-        for (int r = 0; r < kJoinRows; ++r) to[(r0 + r) * D + k] = seq.reads ? from[(r0 + r) * D + k] : 0.0f;
+        for (int r = 0; r < R; ++r) to[(row0 + r) * D + k] = seq.reads ? from[(row0 + r) * D + k] : 0.0f;
     }
+    float2 next[R / 2];
+#pragma unroll
+    for (int r = 0; r < R / 2; ++r) {
+        const float *B = w.summary + at(0) * 2 * D * D + (row0 + 2 * r) * D + k;
+        next[r] = make_float2(B[0], B[D]);
+    }
+    bool bad = false;
     for (int seg = 0; seg + 1 < segs; ++seg) {
-        const int64_t at = (base + seg) * p.heads + h;
-        const float *B = w.summary + at * 2 * D * D;
-        float next[kJoinRows];
+        // next = the state after segment seg
+        float *to = w.first + at(seg + 1) * D * D + row0 * D + k;
 #pragma unroll
-        for (int r = 0; r < kJoinRows; ++r) next[r] = B[(r0 + r) * D + k];
-        if (seg > 0) {
-            const float *M = B + D * D;
-            __syncthreads();
+        for (int r = 0; r < R / 2; ++r) to[2 * r * D] = next[r].x, to[(2 * r + 1) * D] = next[r].y;
+        const int m = seg + 1;  // the segment to pass next
+        if (m + 1 >= segs) break;
+        const int b = m & 1;
 #pragma unroll
-            for (int r = 0; r < kJoinRows; ++r) row[r][k] = S[r];
-            __syncthreads();
-#pragma unroll 16
-            for (int i = 0; i < D; ++i) {
-                const float m = M[i * D + k];
+        for (int r = 0; r < R / 2; ++r) *reinterpret_cast<float2 *>(&sm.row[b][k][r0 + 2 * r]) = next[r];
+        const float *B = w.summary + at(m) * 2 * D * D + row0 * D + k;
 #pragma unroll
-                for (int r = 0; r < kJoinRows; ++r) next[r] = fmaf(row[r][i], m, next[r]);
+        for (int r = 0; r < R / 2; ++r) next[r] = make_float2(B[2 * r * D], B[(2 * r + 1) * D]);
+        bad = !bar_wait(smem_u32(&sm.full[b]), (m - 1) >> 1 & 1, abort);
+        if (__syncthreads_or(bad)) break;
+#pragma unroll 8
+        for (int i = 0; i < D; ++i) {
+            const float x = sm.m[b][i * D + k];
+            const float2 x2 = make_float2(x, x);
+            float4 f[R / 4];
+#pragma unroll
+            for (int r = 0; r < R / 4; ++r) f[r] = *reinterpret_cast<const float4 *>(&sm.row[b][i][r0 + 4 * r]);
+#pragma unroll
+            for (int r = 0; r < R / 4; ++r) {
+                next[2 * r] = fma2(make_float2(f[r].x, f[r].y), x2, next[2 * r]);
+                next[2 * r + 1] = fma2(make_float2(f[r].z, f[r].w), x2, next[2 * r + 1]);
             }
         }
-        float *to = w.first + ((base + seg + 1) * p.heads + h) * D * D;
-#pragma unroll
-        for (int r = 0; r < kJoinRows; ++r) {
-            S[r] = next[r];
-            to[(r0 + r) * D + k] = next[r];
+        __syncthreads();  // M's buffer is read
+        if (threadIdx.x == 0 && m + 3 < segs) fetch(m + 2);
+    }
+    if (sm.abort != 0) {
+        if (threadIdx.x == 0) *reinterpret_cast<volatile int *>(w.ws) = 1;
+        const long long c = clock64();
+        while (clock64() - c < 20000000) {
         }
     }
 }
@@ -1184,13 +1538,20 @@ cudaError_t launch_prepare(const DeltaParams &p, const ChunkPlan &plan, int shor
 }
 
 template <typename T, int D, int kMode>
-cudaError_t launch_walk(const DeltaParams &p, const ChunkPlan &plan, const WalkArgs &w, kda_stream_t stream) {
+cudaError_t launch_walk(const DeltaParams &p, WalkArgs w, int64_t items, kda_stream_t stream) {
     auto *kernel = delta_walk_kernel<T, D, kMode>;
-    const size_t smem = sizeof(WalkSmem<D, kMode>) + 1024;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr size_t smem = sizeof(WalkSmem<D, kMode>) + 1024;
+    static_assert(smem <= 232448, "227 KB per block");
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
     if (e != cudaSuccess) return e;
-    const int64_t items = (plan.split ? plan.segments : p.num_seqs) * p.heads * (kMode == kWalkOut ? 1 : 2);
-    return launch(kernel, dim3((unsigned)items), kWalkThreads, smem, stream, p, w);
+    // The roles' shares add up to exactly this; with fewer they would wait for registers for ever.
+    if (attr.numRegs != Regs<kMode>::launch) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    w.items = items;
+    const int64_t blocks = items < current_sms() ? items : current_sms();
+    return launch(kernel, dim3((unsigned)blocks), kWalkThreads<kMode>, smem, stream, p, w);
 }
 
 template <typename T, int D>
@@ -1211,12 +1572,17 @@ cudaError_t run(const DeltaParams &p, const kda_delta_t *d, const ChunkPlan &pla
     if (plan.split) {
         w.summary = reinterpret_cast<float *>(ws + kHeader + plan.slots * p.heads * slot_bytes(D));
         w.first = w.summary + plan.segments * p.heads * 2 * D * D;
-        e = launch_walk<T, D, kWalkSummary>(p, plan, w, stream);
+        const int64_t marks = p.tokens / w.seg_tokens + 1;  // multiples of a segment's tokens
+        e = launch_walk<T, D, kWalkSummary>(p, w, marks * p.heads, stream);
         if (e != cudaSuccess) return e;
-        e = launch(delta_join_kernel<D>, dim3((unsigned)(p.num_seqs * p.heads), D / kJoinRows), D, 0, stream, p, w);
+        auto *join = delta_join_kernel<D>;
+        e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(JoinSmem<D>));
+        if (e != cudaSuccess) return e;
+        e = launch(join, dim3((unsigned)marks, (unsigned)p.heads, D / kJoinRows), kJoinThreads, sizeof(JoinSmem<D>),
+                   stream, p, w);
         if (e != cudaSuccess) return e;
     }
-    return launch_walk<T, D, kWalkOut>(p, plan, w, stream);
+    return launch_walk<T, D, kWalkOut>(p, w, (plan.split ? plan.segments : p.num_seqs) * p.heads, stream);
 }
 
 }  // namespace
