@@ -48,7 +48,7 @@ struct Slot {
     static constexpr int qw = 0;                              // [q | W hi | W lo token][k]
     static constexpr int k_hi = 3 * kW, k_lo = 4 * kW;        // [k][token]
     static constexpr int a = 5 * kW;                          // [i][j], 64 x 64
-    static constexpr int u = a + kChunk * kChunk * 2;         // fp32 [token][v]
+    static constexpr int u = a + kChunk * kChunk * 2;         // fp32 [token][v ^ 8 (token % 8)]
     static constexpr int decay = u + kChunk * D * 4;          // fp32 [k]: G_63
     static constexpr int scales = decay + D * 4;              // fp32: W, k, q, A unscaling
     static constexpr int bytes = scales + 64;
@@ -153,6 +153,10 @@ __device__ __forceinline__ void block_store(float *to, int ld, const float (&c)[
                 make_float2(sign * c[n][e], sign * c[n][e + 1]);
 }
 
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
 // ------------------------------------------------------------------ prepare
 
 // The sequence that owns slot j of a map f(s) = floor(qsl[s] / unit) + s (the
@@ -191,12 +195,18 @@ struct PrepSmem {
     union {
         struct { __half lk_hi[32][kRow], lk_lo[32][kRow], lq[32][kRow], rk_hi[32][kRow], rk_lo[32][kRow]; } lv;
         struct { __half k_hi[64][kRow], k_lo[64][kRow]; } kg;
+        char w[2 * Slot<D>::kW];  // W's images: a column block's hi and lo rows, block by block
     } x;
-    __half v[64][kRow];
     union {
-        float L[64][68];
-        struct { __half hi[64][72], lo[64][72]; } t;
-    } l;
+        struct {
+            __half v[64][kRow];
+            union {
+                float L[64][68];
+                struct { __half hi[64][72], lo[64][72]; } t;
+            };
+        } l;
+        float u[kChunk * D];  // U as it is stored
+    };
     float T[64][68];
     float tmp[4][16][20];
     __half A[64][72];
@@ -331,30 +341,27 @@ __global__ void __launch_bounds__(256, 2)
     float2 a[8][P];
     float down_k, down_q, down_v;
     {
-        const T *kp = static_cast<const T *>(p.k) + (t0 + b * 8) * p.ks[0] + h * p.ks[1] + lane * C;
-        const T *qp = static_cast<const T *>(p.q) + (t0 + b * 8) * p.qs[0] + h * p.qs[1] + lane * C;
-        const T *vp = static_cast<const T *>(p.v) + (t0 + b * 8) * p.vs[0] + h * p.vs[1] + lane * C;
+        // Rows past the end read the last row instead (no branch between the loads) and are masked.
+        const T *kp = static_cast<const T *>(p.k) + t0 * p.ks[0] + h * p.ks[1] + lane * C;
+        const T *qp = static_cast<const T *>(p.q) + t0 * p.qs[0] + h * p.qs[1] + lane * C;
+        const T *vp = static_cast<const T *>(p.v) + t0 * p.vs[0] + h * p.vs[1] + lane * C;
         Vec<T, C> kv[8], qv[8], vv[8];
         Vec<G, C> gv[8];
         float one[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            one[r] = 0.0f;
-            if (b * 8 + r < n) {
-                if constexpr (kChannelGate)
-                    gv[r] = ld_vec<G, C>(static_cast<const G *>(p.gate) + (t0 + b * 8 + r) * p.gs[0] + h * p.gs[1] + lane * C);
-                else
-                    one[r] = ld_dyn(p.gate, (t0 + b * 8 + r) * p.gs[0] + h * p.gs[1], p.gate_dtype);
-                kv[r] = ld_vec<T, C>(kp + r * p.ks[0]);
-                qv[r] = ld_vec<T, C>(qp + r * p.qs[0]);
-                vv[r] = ld_vec<T, C>(vp + r * p.vs[0]);
-            } else {
+            const int row = min(b * 8 + r, n - 1);
+            if constexpr (kChannelGate)
+                gv[r] = ld_vec<G, C>(static_cast<const G *>(p.gate) + (t0 + row) * p.gs[0] + h * p.gs[1] + lane * C);
+            else
+                one[r] = ld_dyn(p.gate, (t0 + row) * p.gs[0] + h * p.gs[1], p.gate_dtype);
+        }
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    kv[r].v[c] = qv[r].v[c] = vv[r].v[c] = from_f<T>(0.0f);
-                    if constexpr (kChannelGate) gv[r].v[c] = from_f<G>(0.0f);
-                }
-            }
+        for (int r = 0; r < 8; ++r) {
+            const int row = min(b * 8 + r, n - 1);
+            kv[r] = ld_vec<T, C>(kp + row * p.ks[0]);
+            qv[r] = ld_vec<T, C>(qp + row * p.qs[0]);
+            vv[r] = ld_vec<T, C>(vp + row * p.vs[0]);
         }
         if (lane < 8) {
             const int64_t t = t0 + b * 8 + lane;
@@ -387,6 +394,13 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
         for (int c = 0; c < P; ++c)
             *reinterpret_cast<float2 *>(&sm.block_decay[b][lane * C + 2 * c]) = whole[c];
+        if (b * 8 + 8 > n) {  // rows past the end
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (b * 8 + r >= n)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) kv[r].v[c] = qv[r].v[c] = vv[r].v[c] = from_f<T>(0.0f);
+        }
         const uint32_t wk = __reduce_max_sync(0xffffffffu, mag(max_of<T, C>(kv))),
                        wq = __reduce_max_sync(0xffffffffu, mag(max_of<T, C>(qv))),
                        wv = __reduce_max_sync(0xffffffffu, mag(max_of<T, C>(vv)));
@@ -410,7 +424,7 @@ __global__ void __launch_bounds__(256, 2)
                 q[r][c] = __floats2half2_rn(to_f<T>(qv[r].v[2 * c]) * up_q, to_f<T>(qv[r].v[2 * c + 1]) * up_q);
                 f[c] = make_float2(to_f<T>(vv[r].v[2 * c]) * up_v, to_f<T>(vv[r].v[2 * c + 1]) * up_v);
             }
-            store_row<P>(&sm.v[b * 8 + r][lane * C], f);
+            store_row<P>(&sm.l.v[b * 8 + r][lane * C], f);
         }
     }
     // A is kept as A up_q up_k 2^-22, below 2^15 since |A| < 2^(e_q + e_k + 9).
@@ -497,7 +511,7 @@ __global__ void __launch_bounds__(256, 2)
         // kk by hi hi + hi lo + lo hi, qk by hi hi
         if (half == 1) {
             if (b < 4) {  // pair b: rows of k in the tile's first 8 rows, of q in the others
-                float c[4] = {};
+                float c[4] = {}, c1[4] = {}, c2[4] = {};
                 const int lr = lane % 8, piece = lane / 8;
                 const __half *top = (piece & 1) ? sm.x.lv.lq[b * 8 + lr] : sm.x.lv.lk_hi[b * 8 + lr];
                 const __half *low = sm.x.lv.lk_lo[b * 8 + lr];
@@ -511,15 +525,15 @@ __global__ void __launch_bounds__(256, 2)
                     ldsm2(bl, smem_u32(&sm.x.lv.rk_lo[br][kk + bk]));
                     al[1] = al[3] = 0;
                     mma16(c, ah, bh);
-                    mma16(c, al, bh);
+                    mma16(c1, al, bh);
                     ah[1] = ah[3] = 0;
-                    mma16(c, ah, bl);
+                    mma16(c2, ah, bl);
                 }
                 const int i = b * 16 + 8 + g, j = b * 16 + cc;
                 const float f = sm.beta[i] * down_kk;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    sm.l.L[i][j + e] = c[e] * f;
+                    sm.l.L[i][j + e] = (c[e] + (c1[e] + c2[e])) * f;
                     sm.A[i][j + e] = __float2half_rn(c[2 + e] * kDownA);
                 }
             }
@@ -528,7 +542,7 @@ __global__ void __launch_bounds__(256, 2)
             const int m = b / 4;                              // 16-row tile of the left operand
             const int nt = wide ? b % 4 : m * 2 + b / 2 % 2;  // 8-row tile of the right operand
             const bool do_k = wide || b % 2 == 0, do_q = wide || b % 2 == 1;
-            float ck[4] = {}, cq[4] = {};
+            float ck[4] = {}, ck1[4] = {}, ck2[4] = {}, cq[4] = {};
             const int ar = m * 16 + lane % 16, ak = lane / 16 * 8;
             const int br = nt * 8 + lane % 8, bk = (lane / 8 % 2) * 8;
 #pragma unroll
@@ -541,8 +555,8 @@ __global__ void __launch_bounds__(256, 2)
                     ldsm4(al, smem_u32(&sm.x.lv.lk_lo[ar][kk + ak]));
                     ldsm2(bl, smem_u32(&sm.x.lv.rk_lo[br][kk + bk]));
                     mma16(ck, ah, bh);
-                    mma16(ck, al, bh);
-                    mma16(ck, ah, bl);
+                    mma16(ck1, al, bh);
+                    mma16(ck2, ah, bl);
                 }
                 if (do_q) {
                     ldsm4(ah, smem_u32(&sm.x.lv.lq[ar][kk + ak]));
@@ -555,7 +569,7 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = i0 + g + e / 2 * 8, j = j0 + cc + e % 2;
-                if (do_k) sm.l.L[i][j] = ck[e] * (down_kk * sm.beta[i]);
+                if (do_k) sm.l.L[i][j] = (ck[e] + (ck1[e] + ck2[e])) * (down_kk * sm.beta[i]);
                 if (do_q) sm.A[i][j] = __float2half_rn(cq[e] * kDownA);
             }
         }
@@ -714,7 +728,7 @@ __global__ void __launch_bounds__(256, 2)
         for (int x = 0; x < NT; ++x) {
             ldsm2t(bh[x], smem_u32(&sm.x.kg.k_hi[ks * 16 + ar][(b * NT + x) * 8]));
             ldsm2t(bl[x], smem_u32(&sm.x.kg.k_lo[ks * 16 + ar][(b * NT + x) * 8]));
-            ldsm2t(bv[x], smem_u32(&sm.v[ks * 16 + ar][(b * NT + x) * 8]));
+            ldsm2t(bv[x], smem_u32(&sm.l.v[ks * 16 + ar][(b * NT + x) * 8]));
         }
 #pragma unroll
         for (int m = ks; m < 4; ++m) {
@@ -750,9 +764,9 @@ __global__ void __launch_bounds__(256, 2)
     const float up_w = scale_up(top_w), down_u = down_t * down_v;
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-        const int col = (b * NT + x) * 8 + cc;  // rows g + 8 i: the swizzle's row is g
-        char *wo = out + Slot<D>::qw + (col >> 6) * Slot<D>::kBlock + (64 + g) * 128 + (((col >> 3 & 7) ^ g) << 4) + cc * 2;
-        char *uo = out + Slot<D>::u + (g * D + col) * 4;
+        const int col = (b * NT + x) * 8 + cc;  // rows g + 8 i: the swizzles' row is g
+        char *wo = sm.x.w + (col >> 6) * (128 * 128) + g * 128 + (((col >> 3 & 7) ^ g) << 4) + cc * 2;
+        float *uo = &sm.u[g * D + (col ^ (g * 8))];
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -762,9 +776,18 @@ __global__ void __launch_bounds__(256, 2)
                 const int row = m * 16 + e * 4;
                 *reinterpret_cast<uint32_t *>(wo + row * 128) = hi;
                 *reinterpret_cast<uint32_t *>(wo + row * 128 + 64 * 128) = lo;
-                *reinterpret_cast<float2 *>(uo + row * D * 4) =
+                *reinterpret_cast<float2 *>(uo + row * D) =
                     mul2(make_float2(acu[m][x][e], acu[m][x][e + 1]), make_float2(down_u, down_u));
             }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x)
+            bulk_store(out + Slot<D>::qw + x * Slot<D>::kBlock + 64 * 128, smem_u32(sm.x.w) + x * 128 * 128, 128 * 128);
+        bulk_store(out + Slot<D>::u, smem_u32(sm.u), kChunk * D * 4);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
     if (threadIdx.x == 0) {
         float *f = reinterpret_cast<float *>(out + Slot<D>::scales);
@@ -773,6 +796,7 @@ __global__ void __launch_bounds__(256, 2)
         f[2] = down_q;
         f[3] = 0x1p11f * down_q;  // A: times 2^11 down_k
         f[4] = 0x1p11f * down_k;
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the images are in global memory
     }
 }
 
@@ -1141,9 +1165,11 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
                     // V' = U - W S^T
                     float2 V[8];
                     if (x == 0 && row_in) {
-                        const float *u = &sm.u[par][part * 16 * D + v];
+                        const float *u = &sm.u[par][part * 16 * D];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) V[j] = make_float2(u[2 * j * D], u[(2 * j + 1) * D]);
+                        for (int j = 0; j < 8; ++j)
+                            V[j] = make_float2(u[2 * j * D + (v ^ (16 * j & 56))],
+                                               u[(2 * j + 1) * D + (v ^ (16 * j + 8 & 56))]);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) V[j] = make_float2(0.0f, 0.0f);
