@@ -121,36 +121,30 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) 
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
 }
 
-// c += A B for 16 x 16 FP32 blocks in shared memory (rows lda and ldb floats
-// apart), as three tf32 products: unlike halves these need no scaling.
-__device__ __forceinline__ void block_product(float (&c)[2][4], const float *A, int lda, const float *B,
+// c += A B for a 16 x 16 and a 16 x 8 FP32 block in shared memory (rows lda and
+// ldb floats apart), as three tf32 products: unlike halves these need no scaling.
+__device__ __forceinline__ void block_product(float (&c)[3][4], const float *A, int lda, const float *B,
                                               int ldb, int lane) {
     const int g = lane / 4, t = lane % 4;
 #pragma unroll
     for (int k = 0; k < 16; k += 8) {
-        uint32_t ah[4], al[4];
+        uint32_t ah[4], al[4], bh[2], bl[2];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             split_tf32(A[(g + i % 2 * 8) * lda + k + t + i / 2 * 4], ah[i], al[i]);
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            uint32_t bh[2], bl[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) split_tf32(B[(k + t + i * 4) * ldb + n * 8 + g], bh[i], bl[i]);
-            mma8_tf32(c[n], ah, bh);
-            mma8_tf32(c[n], al, bh);
-            mma8_tf32(c[n], ah, bl);
-        }
+        for (int i = 0; i < 2; ++i) split_tf32(B[(k + t + i * 4) * ldb + g], bh[i], bl[i]);
+        mma8_tf32(c[0], ah, bh);
+        mma8_tf32(c[1], al, bh);
+        mma8_tf32(c[2], ah, bl);
     }
 }
-__device__ __forceinline__ void block_store(float *to, int ld, const float (&c)[2][4], float sign, int lane) {
+__device__ __forceinline__ void block_store(float *to, int ld, const float (&c)[3][4], float sign, int lane) {
     const int g = lane / 4, t = lane % 4 * 2;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; e += 2)
-            *reinterpret_cast<float2 *>(to + (g + e * 4) * ld + n * 8 + t) =
-                make_float2(sign * c[n][e], sign * c[n][e + 1]);
+    for (int e = 0; e < 4; e += 2)
+        *reinterpret_cast<float2 *>(to + (g + e * 4) * ld + t) =
+            make_float2(sign * (c[0][e] + (c[1][e] + c[2][e])), sign * (c[0][e + 1] + (c[1][e + 1] + c[2][e + 1])));
 }
 
 __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
@@ -208,12 +202,19 @@ struct PrepSmem {
         float u[kChunk * D];  // U as it is stored
     };
     float T[64][68];
-    float tmp[4][16][20];
+    union {
+        float tmp[4][16][20];
+        float down_t[64];  // unscaling of the rows of T diag(beta)
+    };
     __half A[64][72];
     float block_decay[8][D];
     float beta[64];
-    uint32_t top[4][8];  // per warp: largest |k| (then W), |q|, |v|, T'
+    uint32_t top[3][8];  // per warp: largest |k| (then W), |q|, |v|
 };
+
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
 // Pairs of channels: FP32 in both halves of a 64-bit register pair.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
@@ -316,7 +317,7 @@ __device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0
 // channels of each.
 template <typename T, int D, bool kChannelGate, typename G>
 __global__ void __launch_bounds__(256, 2)
-    delta_prepare_kernel(const __grid_constant__ DeltaParams p, char *ws, int short_len) {
+    delta_prepare_kernel(const __grid_constant__ DeltaParams p, char *ws, int short_len, int ahead) {
     constexpr int C = D / 32, P = C / 2;
     extern __shared__ __align__(1024) char raw_smem[];
     PrepSmem<D> &sm = *reinterpret_cast<PrepSmem<D> *>(raw_smem);
@@ -333,6 +334,20 @@ __global__ void __launch_bounds__(256, 2)
     const int n = (int)min((int64_t)kChunk, seq.end - t0);
     const int b = threadIdx.x / 32, lane = threadIdx.x % 32;
     char *out = ws + kHeader + (slot * p.heads + h) * slot_bytes(D);
+    // The rows that the block after this one on the same SM will read, into L2: `ahead`
+    // tokens further on the same head (in a long sequence; a guess elsewhere).
+    if (ahead > 0) {
+        const int64_t t = t0 + ahead + threadIdx.x / 4;
+        if (t < p.tokens && threadIdx.x % 4 < (int)(D * sizeof(T) / 64)) {
+            const int64_t c = h, o = threadIdx.x % 4 * (64 / sizeof(T));
+            prefetch_l2(static_cast<const T *>(p.k) + t * p.ks[0] + c * p.ks[1] + o);
+            prefetch_l2(static_cast<const T *>(p.q) + t * p.qs[0] + c * p.qs[1] + o);
+            prefetch_l2(static_cast<const T *>(p.v) + t * p.vs[0] + c * p.vs[1] + o);
+            if constexpr (kChannelGate) {
+                prefetch_l2(static_cast<const G *>(p.gate) + t * p.gs[0] + c * p.gs[1] + threadIdx.x % 4 * (64 / sizeof(T)));
+            }
+        }
+    }
 
     // ---- load; rows past the sequence's end are k = q = v = beta = 0, decay 1.
     // k and q stay as halves scaled by a power of two (exact but for values
@@ -661,49 +676,47 @@ __global__ void __launch_bounds__(256, 2)
 
     // ---- T below its diagonal blocks: [X 0; Y Z]^-1 = [X^-1 0; -Z^-1 Y X^-1 Z^-1], for
     // pairs of 16 x 16 blocks, then of 32 x 32
-    if (b < 2) {
-        const int J = 2 * b * 16, I = J + 16;
-        float c[2][4] = {}, d[2][4] = {};
-        block_product(c, &sm.l.L[I][J], 68, &sm.T[J][J], 68, lane);
-        block_store(&sm.tmp[b][0][0], 20, c, 1.0f, lane);
-        __syncwarp();
-        block_product(d, &sm.T[I][I], 68, &sm.tmp[b][0][0], 20, lane);
-        block_store(&sm.T[I][J], 68, d, -1.0f, lane);
-    }
-    __syncthreads();
-    if (b < 4) {
-        const int I = b / 2, J = b % 2;
-        float c[2][4] = {};
+    // A warp computes 8 columns (side) of a block.
+    {
+        const int side = b % 2 * 8;
+        if (b < 4) {
+            const int J = b / 2 * 32, I = J + 16;
+            float c[3][4] = {}, d[3][4] = {};
+            block_product(c, &sm.l.L[I][J], 68, &sm.T[J][J + side], 68, lane);
+            block_store(&sm.tmp[b / 2][0][side], 20, c, 1.0f, lane);
+            __syncwarp();
+            block_product(d, &sm.T[I][I], 68, &sm.tmp[b / 2][0][side], 20, lane);
+            block_store(&sm.T[I][J + side], 68, d, -1.0f, lane);
+        }
+        __syncthreads();
+        const int I = b / 4, J = b / 2 % 2;
+        float c[3][4] = {}, d[3][4] = {};
         for (int m = J; m < 2; ++m)
-            block_product(c, &sm.l.L[32 + I * 16][m * 16], 68, &sm.T[m * 16][J * 16], 68, lane);
-        block_store(&sm.tmp[b][0][0], 20, c, 1.0f, lane);
-    }
-    __syncthreads();
-    if (b < 4) {
-        const int I = b / 2, J = b % 2;
-        float c[2][4] = {};
+            block_product(c, &sm.l.L[32 + I * 16][m * 16], 68, &sm.T[m * 16][J * 16 + side], 68, lane);
+        block_store(&sm.tmp[I * 2 + J][0][side], 20, c, 1.0f, lane);
+        __syncthreads();
         for (int m = 0; m <= I; ++m)
-            block_product(c, &sm.T[32 + I * 16][32 + m * 16], 68, &sm.tmp[m * 2 + J][0][0], 20, lane);
-        block_store(&sm.T[32 + I * 16][J * 16], 68, c, -1.0f, lane);
+            block_product(d, &sm.T[32 + I * 16][32 + m * 16], 68, &sm.tmp[m * 2 + J][0][side], 20, lane);
+        block_store(&sm.T[32 + I * 16][J * 16 + side], 68, d, -1.0f, lane);
     }
     __syncthreads();
 
     // ---- W = T diag(beta) k G and U = T diag(beta) v
     {
         float4 t[4];
-        uint32_t m = 0;
+        float m = 0.0f;
         const int row = threadIdx.x / 4, col = threadIdx.x % 4 * 16;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float4 x = *reinterpret_cast<const float4 *>(&sm.T[row][col + 4 * i]);
             const float4 y = *reinterpret_cast<const float4 *>(&sm.beta[col + 4 * i]);
             t[i] = make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w);
-            m = max(max(max(m, mag(t[i].x)), max(mag(t[i].y), mag(t[i].z))), mag(t[i].w));
+            m = fmaxf(fmaxf(m, fmaxf(fabsf(t[i].x), fabsf(t[i].y))), fmaxf(fabsf(t[i].z), fabsf(t[i].w)));
         }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) sm.top[3][b] = m;
-        __syncthreads();  // also: nobody reads L any more
-        const float up_t = scale_up(top_of(sm.top[3]));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));  // four lanes hold a row: a scale per row
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const float up_t = scale_up(m);
+        if (lane % 4 == 0) sm.down_t[row] = scale_down(m);
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -717,7 +730,6 @@ __global__ void __launch_bounds__(256, 2)
         }
     }
     __syncthreads();
-    const float down_t = scale_down(top_of(sm.top[3]));
     constexpr int NT = D / 64;  // 8-column tiles of a warp
     const int ar = lane % 16, ak = lane / 16 * 8;
     float acc[4][NT][4] = {}, acu[4][NT][4] = {};
@@ -746,22 +758,27 @@ __global__ void __launch_bounds__(256, 2)
         }
     }
     {
-        uint32_t top = 0;
+        float top = 0.0f;
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
-            for (int x = 0; x < NT; ++x)
+            for (int half = 0; half < 2; ++half) {  // rows g and g + 8 of the tile
+                const float down = sm.down_t[m * 16 + half * 8 + g];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    acc[m][x][e] = acc[m][x][e] * down_t * down_k;
-                    top = max(top, mag(acc[m][x][e]));
-                }
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) sm.top[0][b] = top;
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                    for (int e = 2 * half; e < 2 * half + 2; ++e) {
+                        acc[m][x][e] = acc[m][x][e] * down * down_k;
+                        acu[m][x][e] = acu[m][x][e] * down * down_v;
+                        top = fmaxf(top, fabsf(acc[m][x][e]));
+                    }
+            }
+        const uint32_t most = __reduce_max_sync(0xffffffffu, mag(top));
+        if (lane == 0) sm.top[0][b] = most;
     }
     __syncthreads();
     const float top_w = top_of(sm.top[0]);
-    const float up_w = scale_up(top_w), down_u = down_t * down_v;
+    const float up_w = scale_up(top_w);
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
         const int col = (b * NT + x) * 8 + cc;  // rows g + 8 i: the swizzles' row is g
@@ -776,8 +793,7 @@ __global__ void __launch_bounds__(256, 2)
                 const int row = m * 16 + e * 4;
                 *reinterpret_cast<uint32_t *>(wo + row * 128) = hi;
                 *reinterpret_cast<uint32_t *>(wo + row * 128 + 64 * 128) = lo;
-                *reinterpret_cast<float2 *>(uo + row * D) =
-                    mul2(make_float2(acu[m][x][e], acu[m][x][e + 1]), make_float2(down_u, down_u));
+                *reinterpret_cast<float2 *>(uo + row * D) = make_float2(acu[m][x][e], acu[m][x][e + 1]);
             }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1555,12 +1571,16 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
 
 // ------------------------------------------------------------------ host
 
+static_assert(2 * (sizeof(PrepSmem<128>) + 1024) <= 228 * 1024, "two blocks of the preparation per SM");
+
 template <typename T, int D, bool kChannelGate, typename G>
 cudaError_t launch_prepare(const DeltaParams &p, const ChunkPlan &plan, int short_len, char *ws, kda_stream_t stream) {
     auto *kernel = delta_prepare_kernel<T, D, kChannelGate, G>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(PrepSmem<D>));
     if (e != cudaSuccess) return e;
-    return launch(kernel, dim3((unsigned)(plan.slots * p.heads)), 256, sizeof(PrepSmem<D>), stream, p, ws, short_len);
+    // Two blocks per SM run at a time, a token chunk's heads next to each other.
+    const int ahead = (int)(2 * current_sms() / p.heads) * kChunk;
+    return launch(kernel, dim3((unsigned)(plan.slots * p.heads)), 256, sizeof(PrepSmem<D>), stream, p, ws, short_len, ahead);
 }
 
 template <typename T, int D, int kMode>
