@@ -28,12 +28,14 @@ struct Token {
 
 template <typename T, int D, int kGroups, bool kChannelGate, typename G>
 __global__ void __launch_bounds__(kWarps * 32)
-    delta_recurrent_kernel(const __grid_constant__ DeltaParams p, int max_len) {
+    delta_recurrent_kernel(const __grid_constant__ DeltaParams p, int max_len, int *head) {
     constexpr int kRows = kWarps * 4 * kGroups;  // rows of a block
     constexpr int C = D / 32;                    // channels of a lane in the preparation
     constexpr int NV = D / 32;                   // 4-column pieces of a lane's part of a row
     __shared__ Token<D> tok[kBatch];
     dependency_wait();
+    // The head of the chunked path's workspace, before its kernels use it.
+    if (head != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 64) head[threadIdx.x] = 0;
     const int s = blockIdx.x / p.heads, h = blockIdx.x % p.heads;
     const Seq seq = load_seq(p, s);
     if (seq.start >= seq.end || seq.end - seq.start > max_len) return;
@@ -158,42 +160,42 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 template <typename T, int D, int kGroups, bool kChannelGate, typename G>
-cudaError_t launch_groups(const DeltaParams &p, int max_len, kda_stream_t stream) {
+cudaError_t launch_groups(const DeltaParams &p, int max_len, int *head, kda_stream_t stream) {
     const dim3 grid((unsigned)((int64_t)p.num_seqs * p.heads), D / (kWarps * 4 * kGroups));
     return launch(delta_recurrent_kernel<T, D, kGroups, kChannelGate, G>, grid, kWarps * 32, 0, stream,
-                  p, max_len);
+                  p, max_len, head);
 }
 
 template <typename T, int D, bool kChannelGate, typename G>
-cudaError_t launch_rows(const DeltaParams &p, int max_len, kda_stream_t stream) {
+cudaError_t launch_rows(const DeltaParams &p, int max_len, int *head, kda_stream_t stream) {
     // A block of all rows shares one preparation of the tokens; blocks of 32
     // rows spread few (sequence, head) pairs over more SMs.
     if ((int64_t)p.num_seqs * p.heads < 2 * current_sms())
-        return launch_groups<T, D, 1, kChannelGate, G>(p, max_len, stream);
-    return launch_groups<T, D, D / 32, kChannelGate, G>(p, max_len, stream);
+        return launch_groups<T, D, 1, kChannelGate, G>(p, max_len, head, stream);
+    return launch_groups<T, D, D / 32, kChannelGate, G>(p, max_len, head, stream);
 }
 
 template <typename T, int D>
-cudaError_t launch_gate(const DeltaParams &p, bool channel, int max_len, kda_stream_t stream) {
-    if (!channel) return launch_rows<T, D, false, float>(p, max_len, stream);
-    if (p.gate_dtype == KDA_DTYPE_F32) return launch_rows<T, D, true, float>(p, max_len, stream);
-    if (p.gate_dtype == KDA_DTYPE_BF16) return launch_rows<T, D, true, __nv_bfloat16>(p, max_len, stream);
-    return launch_rows<T, D, true, __half>(p, max_len, stream);
+cudaError_t launch_gate(const DeltaParams &p, bool channel, int max_len, int *head, kda_stream_t stream) {
+    if (!channel) return launch_rows<T, D, false, float>(p, max_len, head, stream);
+    if (p.gate_dtype == KDA_DTYPE_F32) return launch_rows<T, D, true, float>(p, max_len, head, stream);
+    if (p.gate_dtype == KDA_DTYPE_BF16) return launch_rows<T, D, true, __nv_bfloat16>(p, max_len, head, stream);
+    return launch_rows<T, D, true, __half>(p, max_len, head, stream);
 }
 
 template <typename T>
-cudaError_t launch_dim(const DeltaParams &p, int head_dim, bool channel, int max_len, kda_stream_t stream) {
-    if (head_dim == 64) return launch_gate<T, 64>(p, channel, max_len, stream);
-    return launch_gate<T, 128>(p, channel, max_len, stream);
+cudaError_t launch_dim(const DeltaParams &p, int head_dim, bool channel, int max_len, int *head, kda_stream_t stream) {
+    if (head_dim == 64) return launch_gate<T, 64>(p, channel, max_len, head, stream);
+    return launch_gate<T, 128>(p, channel, max_len, head, stream);
 }
 
 // Token by token, sequences of at most max_len tokens.
-cudaError_t run_recurrent(const DeltaParams &p, const kda_delta_t *d, int max_len, kda_stream_t stream) {
+cudaError_t run_recurrent(const DeltaParams &p, const kda_delta_t *d, int max_len, int *head, kda_stream_t stream) {
     const bool channel = d->gate_per_channel != 0;
     if (d->x_dtype == KDA_DTYPE_BF16)
-        return launch_dim<__nv_bfloat16>(p, d->head_dim, channel, max_len, stream);
-    if (d->x_dtype == KDA_DTYPE_F16) return launch_dim<__half>(p, d->head_dim, channel, max_len, stream);
-    return launch_dim<float>(p, d->head_dim, channel, max_len, stream);
+        return launch_dim<__nv_bfloat16>(p, d->head_dim, channel, max_len, head, stream);
+    if (d->x_dtype == KDA_DTYPE_F16) return launch_dim<__half>(p, d->head_dim, channel, max_len, head, stream);
+    return launch_dim<float>(p, d->head_dim, channel, max_len, head, stream);
 }
 
 bool strides_ok(const int64_t *s, int64_t quantum) {
@@ -300,13 +302,14 @@ kda_status_t kda_packed_delta_rule(const kda_delta_t *d, int64_t tokens,
     p.null_block_id = null_block_id;
     p.num_seqs = (int)num_seqs;
     p.tokens = tokens;
-    if (!uses_chunks(tokens, d->x_dtype)) return cuda_status(run_recurrent(p, d, INT32_MAX, stream));
+    if (!uses_chunks(tokens, d->x_dtype)) return cuda_status(run_recurrent(p, d, INT32_MAX, nullptr, stream));
     const ChunkPlan plan = chunk_plan(tokens, num_seqs, d->heads, d->head_dim, current_sms());
     if (workspace == nullptr || workspace_bytes < plan.bytes || plan.slots * d->heads > INT32_MAX)
         return KDA_ERR_INVALID_ARG;
     if (!aligned(workspace, 256)) return KDA_ERR_MISALIGNED;
-    cudaError_t e = run_chunked(p, d, plan, kShortLen, workspace, stream);
-    if (e == cudaSuccess) e = run_recurrent(p, d, kShortLen, stream);
+    // The short sequences first: that kernel also zeroes the workspace's head.
+    cudaError_t e = run_recurrent(p, d, kShortLen, static_cast<int *>(workspace), stream);
+    if (e == cudaSuccess) e = run_chunked(p, d, plan, kShortLen, workspace, stream);
     return cuda_status(e);
 }
 
@@ -322,7 +325,7 @@ kda_status_t kda_delta_rule_update(const kda_delta_t *d, int64_t batch, const in
     p.null_block_id = null_block_id;
     p.num_seqs = (int)batch;
     p.tokens = batch;
-    return cuda_status(run_recurrent(p, d, 1, stream));
+    return cuda_status(run_recurrent(p, d, 1, nullptr, stream));
 }
 
 }  // extern "C"

@@ -54,9 +54,30 @@ struct Slot {
     static constexpr int bytes = scales + 64;
 };
 
-// Head of the workspace, written by the preparation: a word set when a wait ran
-// out, then the item counters of the two walks.
+// Head of the workspace, zeroed by the kernel before the preparation: a word
+// set when a wait ran out, the item counters of the two walks, and the lengths
+// of the preparation's two lists of segments.
 constexpr int kHeader = 256;
+enum { kHeadStatus = 0, kHeadSummary = 1, kHeadOut = 2, kHeadFull = 3, kHeadTail = 4 };
+
+// A segment of a sequence, listed by the preparation: those another segment
+// follows (full ones) and the sequences' last ones.
+struct alignas(16) Segment {
+    int begin, rows;  // token rows
+    int slot;         // chunk slot of its first chunk
+    int at;           // segment slot
+    int line;         // state line, -1: the null block
+    int first, last, reads;
+};
+
+struct WalkArgs {
+    char *ws;
+    Segment *full, *tail;
+    float *summary;        // [segment slot][head][2][D][D]: B, M
+    float *start;          // [segment slot][head][D][D]: the state a segment starts from
+    int64_t seg_tokens;    // tokens of a segment (a multiple of 64)
+    int short_len;
+};
 
 __host__ __device__ constexpr int64_t slot_bytes(int D) { return D == 64 ? Slot<64>::bytes : Slot<128>::bytes; }
 
@@ -153,22 +174,9 @@ __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t byt
 
 // ------------------------------------------------------------------ prepare
 
-// The sequence that owns slot j of a map f(s) = floor(qsl[s] / unit) + s (the
-// largest s with f(s) <= j), and j - f(s).
-__device__ __forceinline__ int find_seq(const DeltaParams &p, int64_t j, int64_t unit, int64_t &rest) {
-    int lo = 0, hi = p.num_seqs - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        const int64_t at = max((int64_t)p.query_start_loc[mid], (int64_t)0);
-        if (at / unit + mid <= j) lo = mid;
-        else hi = mid - 1;
-    }
-    rest = j - (max((int64_t)p.query_start_loc[lo], (int64_t)0) / unit + lo);
-    return lo;
-}
-
-// The same for unit kChunk by a whole block of 256 threads: each round narrows
-// the range 256-fold with one load per thread.
+// The sequence that owns chunk slot j: the largest s with f(s) <= j for f(s) =
+// floor(qsl[s] / 64) + s; rest = j - f(s), the chunk's number in it. By a whole block
+// of 256 threads: each round narrows the range 256-fold with one load per thread.
 __device__ __forceinline__ int find_seq_block(const DeltaParams &p, int64_t j, int64_t &rest) {
     int lo = 0, n = p.num_seqs;
     while (n > 1) {
@@ -317,23 +325,37 @@ __device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0
 // channels of each.
 template <typename T, int D, bool kChannelGate, typename G>
 __global__ void __launch_bounds__(256, 2)
-    delta_prepare_kernel(const __grid_constant__ DeltaParams p, char *ws, int short_len, int ahead) {
+    delta_prepare_kernel(const __grid_constant__ DeltaParams p, const __grid_constant__ WalkArgs w, int ahead) {
     constexpr int C = D / 32, P = C / 2;
     extern __shared__ __align__(1024) char raw_smem[];
     PrepSmem<D> &sm = *reinterpret_cast<PrepSmem<D> *>(raw_smem);
     dependency_wait();
-    if (blockIdx.x == 0 && threadIdx.x < 3) reinterpret_cast<int *>(ws)[threadIdx.x] = 0;
     const int64_t slot = blockIdx.x / p.heads;
     const int h = blockIdx.x % p.heads;
     int64_t chunk;
     const int s = find_seq_block(p, slot, chunk);
     const Seq seq = load_seq(p, s);
     const int64_t len = seq.end - seq.start;
-    if (len <= short_len || chunk < 0 || chunk * kChunk >= len) return;
+    if (len <= w.short_len || chunk < 0 || chunk * kChunk >= len) return;
     const int64_t t0 = seq.start + chunk * kChunk;
     const int n = (int)min((int64_t)kChunk, seq.end - t0);
     const int b = threadIdx.x / 32, lane = threadIdx.x % 32;
-    char *out = ws + kHeader + (slot * p.heads + h) * slot_bytes(D);
+    char *out = w.ws + kHeader + (slot * p.heads + h) * slot_bytes(D);
+    if (h == 0 && threadIdx.x == 0 && chunk * kChunk % w.seg_tokens == 0) {  // a segment starts
+        const int64_t seg = chunk * kChunk / w.seg_tokens;
+        const bool last = len - seg * w.seg_tokens <= w.seg_tokens;
+        Segment g;
+        g.begin = (int)t0;
+        g.rows = (int)(last ? seq.end - t0 : w.seg_tokens);
+        g.slot = (int)slot;
+        g.at = (int)(seq.start / w.seg_tokens + s + seg);
+        g.line = (int)seq.line;
+        g.first = seg == 0, g.last = last, g.reads = seq.reads;
+        // At most one entry per chunk slot, so the lists cannot run over.
+        int *head = reinterpret_cast<int *>(w.ws);
+        if (last) w.tail[atomicAdd(head + kHeadTail, 1)] = g;
+        else w.full[atomicAdd(head + kHeadFull, 1)] = g;
+    }
     // The rows that the block after this one on the same SM will read, into L2: `ahead`
     // tokens further on the same head (in a long sequence; a guess elsewhere).
     if (ahead > 0) {
@@ -969,8 +991,7 @@ struct WalkSmem {
 
 // TMEM columns. Of a walk: S as halves (hi, then lo), overwritten by the state's
 // update D once P is done; P = W S^T in two parts (W hi and W lo), the second
-// then overwritten by V' as halves, the first by the second part of o. The
-// first part of o stands before P, so that one MMA writes [o | P | P2]; that
+// then overwritten by V' as halves, the first by the second part of o; that
 // group alternates between two places, so that o may be read a chunk later.
 template <int D, int kMode>
 struct Cols {
@@ -979,61 +1000,26 @@ struct Cols {
     static constexpr int turn = kMode == kWalkOut ? 192 : 0;  // from an even chunk's [o | P | P2] to an odd one's
 };
 
-struct WalkArgs {
-    char *ws;
-    float *summary;        // [segment slot][head][2][D][D]: B, M
-    float *first;          // [segment slot][head][D][D]: the state a segment starts from
-    int64_t seg_tokens;    // tokens of a segment (a multiple of 64)
-    int64_t items;
-    int short_len;
-    int split;             // whether a sequence can have more than one segment
-};
-
-// The segment and head of item i; chunks = 0 where there is nothing to do.
+// Item i: a listed segment and one head. The full segments, the longest, come first.
 template <int D, int kMode>
-__device__ __forceinline__ Item load_item(const DeltaParams &p, const WalkArgs &w, int64_t i) {
+__device__ __forceinline__ Item load_item(const DeltaParams &p, const WalkArgs &w, int64_t i, int full) {
     Item it = {};
-    const int64_t at = i / p.heads;
-    it.head = i % p.heads;
-    int s;
-    int64_t seg = 0;
-    if (kMode == kWalkSummary) {
-        // Every segment but the last of a sequence holds exactly one multiple of seg_tokens.
-        const int64_t t = at * w.seg_tokens;
-        int lo = 0, hi = p.num_seqs - 1;
-        while (lo < hi) {  // the last sequence that starts at or before t
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.query_start_loc[mid] <= t) lo = mid;
-            else hi = mid - 1;
-        }
-        s = lo;
-    } else {
-        s = w.split ? find_seq(p, at, w.seg_tokens, seg) : (int)at;
-    }
-    const Seq seq = load_seq(p, s);
-    const int64_t len = seq.end - seq.start;
-    if (kMode == kWalkSummary) {
-        if (at * w.seg_tokens < seq.start) return it;
-        seg = (at * w.seg_tokens - seq.start) / w.seg_tokens;
-    }
-    if (len <= w.short_len || seg < 0 || seg * w.seg_tokens >= len) return it;
-    const bool last = (seg + 1) * w.seg_tokens >= len;
-    if (kMode == kWalkSummary && last) return it;
-    it.begin = seq.start + seg * w.seg_tokens;
-    it.stop = last ? seq.end : it.begin + w.seg_tokens;
-    it.chunks = (int)((it.stop - it.begin + kChunk - 1) / kChunk);
-    it.slots = w.ws + kHeader +
-        ((seq.start / kChunk + s + seg * (w.seg_tokens / kChunk)) * p.heads + it.head) * slot_bytes(D);
-    const int64_t seg_at = (seq.start / w.seg_tokens + s + seg) * p.heads + it.head;
-    float *line = p.states + (seq.line < 0 ? 0 : seq.line) * p.ss[0] + it.head * p.ss[1];
+    const int at = (int)(i / p.heads);
+    it.head = (int)(i % p.heads);
+    const Segment s = at < full ? w.full[at] : w.tail[at - full];
+    it.begin = s.begin;
+    it.stop = s.begin + s.rows;
+    it.chunks = (s.rows + kChunk - 1) / kChunk;
+    it.slots = w.ws + kHeader + ((int64_t)s.slot * p.heads + it.head) * slot_bytes(D);
+    const int64_t seg_at = (int64_t)s.at * p.heads + it.head;
+    float *line = p.states + (int64_t)max(s.line, 0) * p.ss[0] + it.head * p.ss[1];
     if (kMode == kWalkOut) {
-        if (seg == 0 && last) it.from = seq.reads ? line : nullptr;
-        else it.from = w.first + seg_at * D * D;
-        it.to = last && seq.line >= 0 ? line : nullptr;
+        it.from = !(s.first && s.last) ? w.start + seg_at * D * D : s.reads ? line : nullptr;
+        it.to = s.last && s.line >= 0 ? line : nullptr;
     } else {
-        it.from = seg == 0 && seq.reads ? line : nullptr;
+        it.from = s.first && s.reads ? line : nullptr;
         it.to = w.summary + seg_at * 2 * D * D;
-        it.to_m = seg > 0 ? it.to + D * D : nullptr;
+        it.to_m = s.first ? nullptr : it.to + D * D;
     }
     return it;
 }
@@ -1042,6 +1028,14 @@ __device__ __forceinline__ Item load_item(const DeltaParams &p, const WalkArgs &
 // (which block gets an item changes nothing in its result); the copy warp runs
 // ahead into the next item. Every role keeps a running chunk number n for
 // the rings' parities.
+// Two results rounded to T, the first in the lower half.
+template <typename T>
+__device__ __forceinline__ uint32_t round2(float2 f) {
+    if constexpr (std::is_same<T, __half>::value) return pack2(f);
+    const __nv_bfloat162 h = __float22bfloat162_rn(f);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 template <typename T, int D, int kMode>
 __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
     delta_walk_kernel(const __grid_constant__ DeltaParams p, const __grid_constant__ WalkArgs w) {
@@ -1120,7 +1114,8 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
                 bad |= !bar_wait(bar(kDDone + x), ((x ? n1 : n) - 1) & 1, abort);
                 tc_after();
                 const float *meta = sm.meta[(n - 1) & 1];
-                const float down_k = meta[D + 1], dv = down_v[x];
+                const float both = meta[D + 1] * down_v[x];
+                const float2 down = make_float2(both, both);
 #pragma unroll
                 for (int i = 0; i < CW; i += 16) {
                     uint32_t r[16];
@@ -1129,9 +1124,8 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         const float4 gs = *reinterpret_cast<const float4 *>(meta + part * CW + i + j);
-                        const float2 dk2 = make_float2(down_k, down_k), dv2 = make_float2(dv, dv);
-                        const float2 x0 = mul2(mul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), dk2), dv2);
-                        const float2 x1 = mul2(mul2(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), dk2), dv2);
+                        const float2 x0 = mul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), down);
+                        const float2 x1 = mul2(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), down);
                         S[x][(i + j) / 2] = fma2(S[x][(i + j) / 2], make_float2(gs.x, gs.y), x0);
                         S[x][(i + j) / 2 + 1] = fma2(S[x][(i + j) / 2 + 1], make_float2(gs.z, gs.w), x1);
                     }
@@ -1194,7 +1188,8 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
                     tc_after();
                     {
                         const float down_w = sm.meta[par][D];
-                        const float2 dw = make_float2(down_w, down_w), ds = make_float2(-down_s[x], -down_s[x]);
+                        const float both = -down_w * down_s[x];
+                        const float2 down = make_float2(both, both);
 #pragma unroll
                         for (int j = 0; j < 16; j += 8) {
                             uint32_t r0[8], r1[8];
@@ -1205,7 +1200,7 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
                             for (int i = 0; i < 8; i += 2) {
                                 const float2 f = __fadd2_rn(make_float2(__uint_as_float(r0[i]), __uint_as_float(r0[i + 1])),
                                                             make_float2(__uint_as_float(r1[i]), __uint_as_float(r1[i + 1])));
-                                V[(i + j) / 2] = fma2(mul2(f, dw), ds, V[(i + j) / 2]);
+                                V[(i + j) / 2] = fma2(f, down, V[(i + j) / 2]);
                             }
                         }
                     }
@@ -1279,8 +1274,8 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
                     if (meet_any<2, 128>(bad)) { bad = true; break; }  // also: sm.o is free
                     tc_after();
                     const float *meta = sm.meta[par];
-                    const float f1 = meta[D + 2] * p.scale, f2 = meta[D + 3] * p.scale, f3 = meta[D + 4];
-                    const float ds = sm.row_scale[0][n & 3][v], dv = sm.row_scale[1][n & 3][v];
+                    const float f1 = meta[D + 2] * sm.row_scale[0][n & 3][v] * p.scale;
+                    const float f2 = meta[D + 3] * (meta[D + 4] * sm.row_scale[1][n & 3][v]) * p.scale;
 #pragma unroll
                     for (int i = 0; i < 64; i += 16) {
                         uint32_t r[16], x[16];
@@ -1289,9 +1284,13 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
                         tc_wait_ld();
                         if (v < D)
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                reinterpret_cast<T *>(sm.o[i + j])[v] =
-                                    from_f<T>(__uint_as_float(r[j]) * f1 * ds + __uint_as_float(x[j]) * f2 * f3 * dv);
+                            for (int j = 0; j < 16; j += 2) {
+                                const float2 f = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(f2, f2),
+                                                      mul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), make_float2(f1, f1)));
+                                const uint32_t two = round2<T>(f);
+                                sm.o[i + j][v] = (uint16_t)two;
+                                sm.o[i + j + 1][v] = (uint16_t)(two >> 16);
+                            }
                     }
                     tc_before();
                     __syncwarp();
@@ -1319,6 +1318,7 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
             // ---- the thread that issues to the tensor core
             constexpr int kBlock = Sm::kRows * 128;  // an image's column block of 64
             constexpr int kQ = kOut ? 64 : 0;        // rows before W
+            constexpr bool kWide = !std::is_same<T, __nv_bfloat16>::value;  // o takes the operands' lo halves too
             uint32_t n = 0, n1 = 0;
             bool ok = true;
             for (uint32_t k = 0; ok; ++k) {
@@ -1340,16 +1340,22 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
                         if (!ok) break;
                         tc_after();
                         const uint32_t base = tmem + x * Col::walk, acc = base + par * Col::turn;
-                        // S hi [q | W hi | W lo]^T, then S lo [q | W hi]^T
+                        // S hi [W hi | W lo]^T, then S lo [W hi]^T
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
-                            tc_mma(acc + (kOut ? Col::o1 : Col::p), base + Col::s + i * 8,
-                                   operand_desc(wi + i / 4 * kBlock + i % 4 * 32), instr_desc(kQ + 128), i != 0);
+                            tc_mma(acc + Col::p, base + Col::s + i * 8,
+                                   operand_desc(wi + kQ * 128 + i / 4 * kBlock + i % 4 * 32), instr_desc(128), i != 0);
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
-                            tc_mma(acc + (kOut ? Col::o1 : Col::p), base + Col::s + D / 2 + i * 8,
-                                   operand_desc(wi + i / 4 * kBlock + i % 4 * 32), instr_desc(kQ + 64), true);
+                            tc_mma(acc + Col::p, base + Col::s + D / 2 + i * 8,
+                                   operand_desc(wi + kQ * 128 + i / 4 * kBlock + i % 4 * 32), instr_desc(64), true);
                         tc_commit(bar(kPDone + x));
+                        if (kOut) {  // S hi [q]^T, for an fp16 result S lo too, while V' is made
+#pragma unroll
+                            for (int i = 0; i < (kWide ? 2 : 1) * (D / 16); ++i)
+                                tc_mma(acc + Col::o1, base + Col::s + i * 8,
+                                       operand_desc(wi + i % (D / 16) / 4 * kBlock + i % 4 * 32), instr_desc(64), i != 0);
+                        }
                     }
                     if (!ok) break;
                     tc_commit(bar(kWEmpty + par));
@@ -1376,7 +1382,7 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
                         ok = bar_wait(bar(kAFull), par, abort);
                         if (!ok) break;
                         const uint32_t ai = smem_u32(sm.a), acc = tmem + par * Col::turn;
-                        constexpr int kTerms = !std::is_same<T, __nv_bfloat16>::value ? 8 : 4;
+                        constexpr int kTerms = kWide ? 8 : 4;
 #pragma unroll
                         for (int i = 0; i < kTerms; ++i)  // V' hi, and for an fp16 result V' lo
                             tc_mma(acc + Col::o2, acc + Col::v + (i / 4) * 32 + i % 4 * 8,
@@ -1392,15 +1398,16 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
         const int64_t step = (int64_t)p.heads * slot_bytes(D);
         uint32_t n = 0, k = 0;
         bool ok = true;
-        int *counter = reinterpret_cast<int *>(w.ws) + (kOut ? 2 : 1);
+        int *head = reinterpret_cast<int *>(w.ws), *counter = head + (kOut ? kHeadOut : kHeadSummary);
+        const int full = head[kHeadFull];
+        const int64_t items = (int64_t)(full + (kOut ? head[kHeadTail] : 0)) * p.heads;
         int64_t next = blockIdx.x;
         while (ok) {
             const int64_t i = next;
-            if (i < w.items) next = gridDim.x + (int64_t)atomicAdd(counter, 1);
             Item it = {};
-            if (i < w.items) {
-                it = load_item<D, kMode>(p, w, i);
-                if (it.chunks == 0) continue;
+            if (i < items) {
+                next = gridDim.x + (int64_t)atomicAdd(counter, 1);
+                it = load_item<D, kMode>(p, w, i, full);
             }
             if (k >= 2) ok = bar_wait(bar(kItemEmpty + (k & 1)), (k >> 1 & 1) ^ 1, abort);
             if (!ok) break;
@@ -1450,7 +1457,7 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
     if (sm.abort != 0) {
         // A wait ran out (never in a correct run): say so, and give the copies in
         // flight time to land before the block's shared memory is given back.
-        if (threadIdx.x == 0) *reinterpret_cast<volatile int *>(w.ws) = 1;
+        if (threadIdx.x == 0) reinterpret_cast<volatile int *>(w.ws)[kHeadStatus] = 1;
         const long long t = clock64();
         while (clock64() - t < 20000000) {
         }
@@ -1463,16 +1470,18 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
 
 // ------------------------------------------------------------------ join
 
-// For each sequence of several segments: first[0] = the cached state (the walk
-// of the last segment overwrites it), first[seg + 1] = (seg ? first[seg] M[seg]
+// For each sequence of several segments: start[0] = the cached state (the walk
+// of the last segment overwrites it), start[seg + 1] = (seg ? start[seg] M[seg]
 // : 0) + B[seg], segment by segment. A block takes kJoinRows rows of one
 // head's state; M comes by bulk copies, one segment ahead.
 constexpr int kJoinRows = 16, kJoinThreads = 256;
 
 template <int D>
 struct JoinSmem {
+    static constexpr int kSplits = kJoinThreads / (D / 4) / 2;  // parts of the sum over i: 4 (D = 128), 8
     float m[2][D * D];
-    float row[2][D][kJoinRows];
+    float row[2][D][kJoinRows];           // the state, transposed
+    float part[kSplits][kJoinRows][D];    // partial products
     uint64_t full[2];
     int abort;
 };
@@ -1480,9 +1489,10 @@ struct JoinSmem {
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_constant__ DeltaParams p,
                                                                  const __grid_constant__ WalkArgs w) {
-    constexpr int R = kJoinRows * D / kJoinThreads;  // rows of a thread
+    using Sm = JoinSmem<D>;
+    constexpr int kOwn = kJoinRows * D / kJoinThreads;  // values of a thread: consecutive rows of a column
     extern __shared__ __align__(1024) char raw_smem[];
-    JoinSmem<D> &sm = *reinterpret_cast<JoinSmem<D> *>(raw_smem);
+    Sm &sm = *reinterpret_cast<Sm *>(raw_smem);
     dependency_wait();
     // The sequence that holds token (multiple of seg_tokens) number blockIdx.x, if that is
     // the first multiple in it: every sequence of several segments holds one.
@@ -1499,10 +1509,12 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
     if (t < seq.start || t - seq.start >= w.seg_tokens || len <= w.short_len || len <= w.seg_tokens) return;
     const int segs = (int)((len + w.seg_tokens - 1) / w.seg_tokens);
     const int64_t base = seq.start / w.seg_tokens + lo;
-    const int k = threadIdx.x % D, r0 = threadIdx.x / D * R, row0 = blockIdx.z * kJoinRows + r0;
+    const int tid = threadIdx.x, k = tid % D, r0 = tid / D * kOwn, row0 = blockIdx.z * kJoinRows + r0;
+    // In the product: 4 columns, 8 rows and one part of the sum.
+    const int c4 = tid % (D / 4) * 4, r8 = tid / (D / 4) % 2 * 8, split = tid / (D / 4) / 2;
     auto at = [&](int seg) { return (base + seg) * p.heads + h; };
     volatile int *abort = &sm.abort;
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         sm.abort = 0;
         bar_init(smem_u32(&sm.full[0]), 1);
         bar_init(smem_u32(&sm.full[1]), 1);
@@ -1515,54 +1527,65 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
         bar_expect(bar, D * D * 4);
         bulk_load(smem_u32(sm.m[seg & 1]), w.summary + (at(seg) * 2 + 1) * D * D, D * D * 4, bar);
     };
-    if (threadIdx.x == 0 && segs > 2) fetch(1);
-    if (threadIdx.x == 0 && segs > 3) fetch(2);
+    if (tid == 0 && segs > 2) fetch(1);
+    if (tid == 0 && segs > 3) fetch(2);
     {
         const float *from = p.states + (seq.reads ? seq.line : 0) * p.ss[0] + h * p.ss[1];
-        float *to = w.first + at(0) * D * D;
+        float *to = w.start + at(0) * D * D;
 #pragma unroll
-        for (int r = 0; r < R; ++r) to[(row0 + r) * D + k] = seq.reads ? from[(row0 + r) * D + k] : 0.0f;
+        for (int r = 0; r < kOwn; ++r) to[(row0 + r) * D + k] = seq.reads ? from[(row0 + r) * D + k] : 0.0f;
     }
-    float2 next[R / 2];
+    float S[kOwn];  // the state after the segments so far
 #pragma unroll
-    for (int r = 0; r < R / 2; ++r) {
-        const float *B = w.summary + at(0) * 2 * D * D + (row0 + 2 * r) * D + k;
-        next[r] = make_float2(B[0], B[D]);
-    }
+    for (int r = 0; r < kOwn; ++r) S[r] = w.summary[at(0) * 2 * D * D + (row0 + r) * D + k];
     bool bad = false;
-    for (int seg = 0; seg + 1 < segs; ++seg) {
-        // next = the state after segment seg
-        float *to = w.first + at(seg + 1) * D * D + row0 * D + k;
+    for (int m = 1; m < segs; ++m) {  // S: before segment m
+        float *to = w.start + at(m) * D * D + row0 * D + k;
 #pragma unroll
-        for (int r = 0; r < R / 2; ++r) to[2 * r * D] = next[r].x, to[(2 * r + 1) * D] = next[r].y;
-        const int m = seg + 1;  // the segment to pass next
+        for (int r = 0; r < kOwn; ++r) to[r * D] = S[r];
         if (m + 1 >= segs) break;
         const int b = m & 1;
 #pragma unroll
-        for (int r = 0; r < R / 2; ++r) *reinterpret_cast<float2 *>(&sm.row[b][k][r0 + 2 * r]) = next[r];
+        for (int r = 0; r < kOwn; ++r) sm.row[b][k][r0 + r] = S[r];
         const float *B = w.summary + at(m) * 2 * D * D + row0 * D + k;
 #pragma unroll
-        for (int r = 0; r < R / 2; ++r) next[r] = make_float2(B[2 * r * D], B[(2 * r + 1) * D]);
+        for (int r = 0; r < kOwn; ++r) S[r] = B[r * D];
         bad = !bar_wait(smem_u32(&sm.full[b]), (m - 1) >> 1 & 1, abort);
         if (__syncthreads_or(bad)) break;
+        float2 acc[4][4] = {};  // [column][pair of rows]
+        constexpr int kLen = D / Sm::kSplits;
 #pragma unroll 8
-        for (int i = 0; i < D; ++i) {
-            const float x = sm.m[b][i * D + k];
-            const float2 x2 = make_float2(x, x);
-            float4 f[R / 4];
+        for (int j = 0; j < kLen; ++j) {
+            const int i = split * kLen + j;
+            const float4 x = *reinterpret_cast<const float4 *>(&sm.m[b][i * D + c4]);
+            const float4 f = *reinterpret_cast<const float4 *>(&sm.row[b][i][r8]);
+            const float4 g = *reinterpret_cast<const float4 *>(&sm.row[b][i][r8 + 4]);
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+            const float2 rows[4] = {make_float2(f.x, f.y), make_float2(f.z, f.w), make_float2(g.x, g.y), make_float2(g.z, g.w)};
 #pragma unroll
-            for (int r = 0; r < R / 4; ++r) f[r] = *reinterpret_cast<const float4 *>(&sm.row[b][i][r0 + 4 * r]);
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int r = 0; r < R / 4; ++r) {
-                next[2 * r] = fma2(make_float2(f[r].x, f[r].y), x2, next[2 * r]);
-                next[2 * r + 1] = fma2(make_float2(f[r].z, f[r].w), x2, next[2 * r + 1]);
-            }
+                for (int r = 0; r < 4; ++r) acc[c][r] = fma2(rows[r], make_float2(xs[c], xs[c]), acc[c][r]);
         }
-        __syncthreads();  // M's buffer is read
-        if (threadIdx.x == 0 && m + 3 < segs) fetch(m + 2);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            *reinterpret_cast<float4 *>(&sm.part[split][r8 + 2 * r][c4]) =
+                make_float4(acc[0][r].x, acc[1][r].x, acc[2][r].x, acc[3][r].x);
+            *reinterpret_cast<float4 *>(&sm.part[split][r8 + 2 * r + 1][c4]) =
+                make_float4(acc[0][r].y, acc[1][r].y, acc[2][r].y, acc[3][r].y);
+        }
+        __syncthreads();  // M's buffer is read, the parts are written
+        if (tid == 0 && m + 3 < segs) fetch(m + 2);
+#pragma unroll
+        for (int r = 0; r < kOwn; ++r) {
+            float sum = sm.part[0][r0 + r][k];
+#pragma unroll
+            for (int x = 1; x < Sm::kSplits; ++x) sum += sm.part[x][r0 + r][k];
+            S[r] += sum;
+        }
     }
     if (sm.abort != 0) {
-        if (threadIdx.x == 0) *reinterpret_cast<volatile int *>(w.ws) = 1;
+        if (tid == 0) reinterpret_cast<volatile int *>(w.ws)[kHeadStatus] = 1;
         const long long c = clock64();
         while (clock64() - c < 20000000) {
         }
@@ -1574,17 +1597,17 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
 static_assert(2 * (sizeof(PrepSmem<128>) + 1024) <= 228 * 1024, "two blocks of the preparation per SM");
 
 template <typename T, int D, bool kChannelGate, typename G>
-cudaError_t launch_prepare(const DeltaParams &p, const ChunkPlan &plan, int short_len, char *ws, kda_stream_t stream) {
+cudaError_t launch_prepare(const DeltaParams &p, const ChunkPlan &plan, const WalkArgs &w, kda_stream_t stream) {
     auto *kernel = delta_prepare_kernel<T, D, kChannelGate, G>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(PrepSmem<D>));
     if (e != cudaSuccess) return e;
     // Two blocks per SM run at a time, a token chunk's heads next to each other.
     const int ahead = (int)(2 * current_sms() / p.heads) * kChunk;
-    return launch(kernel, dim3((unsigned)(plan.slots * p.heads)), 256, sizeof(PrepSmem<D>), stream, p, ws, short_len, ahead);
+    return launch(kernel, dim3((unsigned)(plan.slots * p.heads)), 256, sizeof(PrepSmem<D>), stream, p, w, ahead);
 }
 
 template <typename T, int D, int kMode>
-cudaError_t launch_walk(const DeltaParams &p, WalkArgs w, int64_t items, kda_stream_t stream) {
+cudaError_t launch_walk(const DeltaParams &p, const WalkArgs &w, int64_t items, kda_stream_t stream) {
     auto *kernel = delta_walk_kernel<T, D, kMode>;
     constexpr size_t smem = sizeof(WalkSmem<D, kMode>) + 1024;
     static_assert(smem <= 232448, "227 KB per block");
@@ -1595,7 +1618,6 @@ cudaError_t launch_walk(const DeltaParams &p, WalkArgs w, int64_t items, kda_str
     if (attr.numRegs != Regs<kMode>::launch) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    w.items = items;
     const int64_t blocks = items < current_sms() ? items : current_sms();
     return launch(kernel, dim3((unsigned)blocks), kWalkThreads<kMode>, smem, stream, p, w);
 }
@@ -1603,21 +1625,21 @@ cudaError_t launch_walk(const DeltaParams &p, WalkArgs w, int64_t items, kda_str
 template <typename T, int D>
 cudaError_t run(const DeltaParams &p, const kda_delta_t *d, const ChunkPlan &plan, int short_len, char *ws,
                 kda_stream_t stream) {
-    cudaError_t e;
-    if (!d->gate_per_channel) e = launch_prepare<T, D, false, float>(p, plan, short_len, ws, stream);
-    else if (d->gate_dtype == KDA_DTYPE_F32) e = launch_prepare<T, D, true, float>(p, plan, short_len, ws, stream);
-    else if (d->gate_dtype == KDA_DTYPE_BF16)
-        e = launch_prepare<T, D, true, __nv_bfloat16>(p, plan, short_len, ws, stream);
-    else e = launch_prepare<T, D, true, __half>(p, plan, short_len, ws, stream);
-    if (e != cudaSuccess) return e;
     WalkArgs w = {};
     w.ws = ws;
     w.seg_tokens = (int64_t)plan.seg_chunks * kChunk;
     w.short_len = short_len;
-    w.split = plan.split;
+    w.full = reinterpret_cast<Segment *>(ws + kHeader + plan.slots * p.heads * slot_bytes(D));
+    w.tail = w.full + plan.slots;
+    cudaError_t e;
+    if (!d->gate_per_channel) e = launch_prepare<T, D, false, float>(p, plan, w, stream);
+    else if (d->gate_dtype == KDA_DTYPE_F32) e = launch_prepare<T, D, true, float>(p, plan, w, stream);
+    else if (d->gate_dtype == KDA_DTYPE_BF16) e = launch_prepare<T, D, true, __nv_bfloat16>(p, plan, w, stream);
+    else e = launch_prepare<T, D, true, __half>(p, plan, w, stream);
+    if (e != cudaSuccess) return e;
     if (plan.split) {
-        w.summary = reinterpret_cast<float *>(ws + kHeader + plan.slots * p.heads * slot_bytes(D));
-        w.first = w.summary + plan.segments * p.heads * 2 * D * D;
+        w.summary = reinterpret_cast<float *>(w.tail + plan.slots);
+        w.start = w.summary + plan.segments * p.heads * 2 * D * D;
         const int64_t marks = p.tokens / w.seg_tokens + 1;  // multiples of a segment's tokens
         e = launch_walk<T, D, kWalkSummary>(p, w, marks * p.heads, stream);
         if (e != cudaSuccess) return e;
@@ -1637,14 +1659,16 @@ ChunkPlan chunk_plan(int64_t tokens, int64_t num_seqs, int64_t heads, int head_d
     ChunkPlan c = {};
     c.slots = tokens / kChunk + num_seqs;
     const int64_t chunks = (tokens + kChunk - 1) / kChunk;  // of one sequence, at most
-    // One wave of segments if one sequence had all tokens, of at least 4 chunks.
+    // One wave of segments if one sequence had all tokens, of at least 8 chunks: a split
+    // sequence is walked twice and pays the join.
     const int64_t parts = sms / heads > 1 ? sms / heads : 1;
     int64_t seg = (chunks + parts - 1) / parts;
-    if (seg < 4) seg = 4;
+    if (seg < 8) seg = 8;
+    c.split = chunks > 16 && chunks > seg;
+    if (!c.split) seg = chunks > 0 ? chunks : 1;
     c.seg_chunks = (int)seg;
-    c.split = chunks > seg;
     c.segments = c.split ? tokens / (seg * kChunk) + num_seqs : num_seqs;
-    c.bytes = kHeader + c.slots * heads * slot_bytes(head_dim);
+    c.bytes = kHeader + c.slots * heads * slot_bytes(head_dim) + 2 * c.slots * (int64_t)sizeof(Segment);
     if (c.split) c.bytes += c.segments * heads * 3 * head_dim * head_dim * 4;
     return c;
 }
