@@ -5,6 +5,7 @@ conversion only; every step runs in the library's CUDA kernels."""
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -20,6 +21,7 @@ KDA_NORM_GATE_SILU = 2
 
 _P, _I64, _I32, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 _Pair = _I64 * 2
+_SixLong = _I64 * 6
 
 
 class KdaDelta(ctypes.Structure):
@@ -42,7 +44,7 @@ def _lib() -> ctypes.CDLL:
     global _declared
     h = lib()
     if _declared is not h:
-        D = ctypes.POINTER(KdaDelta)
+        D = _P  # a KdaDelta by reference, or its bytes
         h.kda_delta_check.argtypes = [D]
         h.kda_packed_delta_rule_workspace.argtypes = [_I64, _I64, _I64, _I32, _I32, _I32,
                                                       ctypes.POINTER(_I64)]
@@ -71,11 +73,38 @@ def _check(status: int) -> None:
         raise KdaError(status, what)
 
 
-def _stream_of(stream, device) -> int:
-    """The raw handle: `stream`, or torch's current stream of the tensors' device."""
+def _raw_stream(stream, index: int) -> int:
+    """The raw handle: `stream`, or torch's current stream of device `index`."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current_raw_stream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+# torch.cuda.current_stream builds a Stream object; the raw handle is all that is needed.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class _Here:
+    """A context that does nothing: the tensors' device is the current one already."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *_):
+        return None
+
+
+_here = _Here()
+
+
+def _on_device(index: int):
+    return _here if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+def _empty_like(t: torch.Tensor, stream) -> torch.Tensor:
+    """A contiguous tensor of t's shape and type for a call on `stream`."""
+    return t.new_empty(t.shape) if stream is None else _empty_on(stream, t.shape, t.dtype, t.device)
 
 
 def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
@@ -88,6 +117,12 @@ def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+# The checks of the wrappers come twice: one expression that holds for ordinary
+# arguments, and, where it does not, the step-by-step form that says what is wrong
+# (or finds that nothing is).  A decode step's calls are too short to spend the
+# step-by-step form on.
+
+
 def _same_device(lead: str, **tensors) -> torch.device:
     """Every tensor on the CUDA device of `lead` (there is no CPU path)."""
     dev = tensors[lead].device
@@ -97,11 +132,6 @@ def _same_device(lead: str, **tensors) -> torch.device:
         if t is not None and t.device != dev:
             raise ValueError(f"{name} is on {t.device}, {lead} on {dev}")
     return dev
-
-
-def _strides(t: torch.Tensor, n: int):
-    """The first n strides; 0 for an axis of one entry, whose stride is never used."""
-    return [t.stride(i) if t.size(i) > 1 else 0 for i in range(n)]
 
 
 def _written(name: str, t) -> None:
@@ -118,8 +148,8 @@ def _vector32(name: str, t, shapes) -> None:
                          f"{' or '.join(str(s) for s in shapes)}, not {t.dtype} {tuple(t.shape)}")
 
 
-def _delta(q, k, v, gate, beta, states, scale, a_log, dt_bias, beta_logits, out):
-    """The checked KdaDelta of these tensors (out's pointer and strides left out)."""
+def _explain_delta(q, k, v, gate, beta, states, a_log, dt_bias, out, metadata) -> None:
+    """Raises what is wrong with the arguments of the delta rule, if anything."""
     if q.dim() != 3 or q.dtype not in _DTYPES:
         raise ValueError("q must be (tokens, heads, head_dim) in bf16, fp16 or fp32")
     tokens, heads, dim = q.shape
@@ -153,23 +183,70 @@ def _delta(q, k, v, gate, beta, states, scale, a_log, dt_bias, beta_logits, out)
         raise ValueError("dt_bias needs a_log")
     _vector32("a_log", a_log, [(heads,)])
     _vector32("dt_bias", dt_bias, [(heads, dim), (heads * dim,)] if channel else [(heads,)])
-    d = KdaDelta()
-    d.x_dtype, d.gate_dtype, d.beta_dtype = (_DTYPES[t.dtype] for t in (q, gate, beta))
-    d.gate_kind = KDA_GATE_LOG if a_log is None else KDA_GATE_SOFTPLUS
-    d.gate_per_channel = int(channel)
-    d.beta_kind = KDA_BETA_SIGMOID if beta_logits else KDA_BETA_PLAIN
-    d.heads, d.head_dim = heads, dim
-    d.scale = dim ** -0.5 if scale is None else float(scale)
-    d.q, d.k, d.v, d.gate, d.beta = (t.data_ptr() for t in (q, k, v, gate, beta))
-    d.a_log, d.dt_bias, d.states = _ptr(a_log), _ptr(dt_bias), states.data_ptr()
-    for name, t in (("q_stride", q), ("k_stride", k), ("v_stride", v), ("gate_stride", gate),
-                    ("beta_stride", beta), ("state_stride", states)):
-        setattr(d, name, _Pair(*_strides(t, 2)))
-    return d
+    seqs = tokens
+    if "query_start_loc" in metadata:
+        seqs = max(metadata["query_start_loc"].numel() - 1, 0)
+        _check_vector("query_start_loc", metadata["query_start_loc"], 0, (torch.int32,))
+    _check_vector("cache_indices", metadata["cache_indices"], seqs, (torch.int32,), strided=True)
+    if "has_initial_state" in metadata:
+        _check_vector("has_initial_state", metadata["has_initial_state"], seqs,
+                      (torch.bool, torch.uint8))
+    _same_device("q", q=q, k=k, v=v, gate=gate, beta=beta, states=states, a_log=a_log,
+                 dt_bias=dt_bias, out=out, **metadata)
 
 
-def _set_out(d: KdaDelta, out: torch.Tensor) -> None:
-    d.out, d.out_stride = out.data_ptr(), _Pair(*_strides(out, 2))
+def _delta_ok(q, k, v, gate, beta, states, a_log, dt_bias, out, cache_indices, seqs) -> bool:
+    """Whether these are ordinary arguments (shapes of more than one token are not asked for)."""
+    shape, dt, index = q.shape, q.dtype, q.get_device()
+    if len(shape) != 3 or index < 0 or dt not in _DTYPES:
+        return False
+    tokens, heads, dim = shape
+    per_channel = gate.shape == shape
+    s, g = states.stride(), gate.stride()
+    return (tokens > 0 and k.dtype is dt and v.dtype is dt and k.shape == shape
+            and v.shape == shape and q.stride(2) == k.stride(2) == v.stride(2) == 1
+            and (out is None or (out.dtype is dt and out.shape == shape and out.is_contiguous()
+                                 and out.get_device() == index))
+            and (g[2] == 1 if per_channel else gate.shape == (tokens, heads))
+            and gate.dtype in _DTYPES and beta.dtype in _DTYPES and beta.shape == (tokens, heads)
+            and states.dtype is torch.float32 and states.shape[1:] == (heads, dim, dim)
+            and s[3] == 1 and s[2] == dim and s[0] > 0 and s[1] > 0
+            and cache_indices.dtype is torch.int32 and cache_indices.dim() == 1
+            and cache_indices.stride(0) > 0 and cache_indices.numel() >= seqs
+            and (a_log is None or (a_log.dtype is torch.float32 and a_log.shape == (heads,)
+                                   and a_log.is_contiguous() and a_log.get_device() == index))
+            and (dt_bias is None or (
+                a_log is not None and dt_bias.dtype is torch.float32
+                and dt_bias.shape == ((heads, dim) if per_channel else (heads,))
+                and dt_bias.is_contiguous() and dt_bias.get_device() == index))
+            and k.get_device() == index and v.get_device() == index
+            and gate.get_device() == index and beta.get_device() == index
+            and states.get_device() == index and cache_indices.get_device() == index)
+
+
+_pack_delta = struct.Struct("8iqfi9Q15q").pack  # KdaDelta, field by field
+
+
+def _delta(q, k, v, gate, beta, states, scale, a_log, dt_bias, beta_logits, out,
+           cache_indices) -> bytes:
+    """The bytes of the KdaDelta that describes checked tensors.  The stride of an
+    axis of one entry is never used and given as 0."""
+    tokens, heads, dim = q.shape
+    many, more = tokens > 1, heads > 1
+    strides = []
+    for t in (q, k, v, gate, beta, out):
+        s = t.stride()
+        strides.append(s[0] if many else 0)
+        strides.append(s[1] if more else 0)
+    s = states.stride()
+    return _pack_delta(
+        0, _DTYPES[q.dtype], _DTYPES[gate.dtype], _DTYPES[beta.dtype],
+        KDA_GATE_LOG if a_log is None else KDA_GATE_SOFTPLUS, gate.dim() - 2,
+        KDA_BETA_SIGMOID if beta_logits else KDA_BETA_PLAIN, dim, heads,
+        dim ** -0.5 if scale is None else scale, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        gate.data_ptr(), beta.data_ptr(), _ptr(a_log) or 0, _ptr(dt_bias) or 0, states.data_ptr(),
+        out.data_ptr(), *strides, s[0] if states.size(0) > 1 else 0, s[1] if more else 0,
+        cache_indices.stride(0) if cache_indices.numel() > 1 else 1)
 
 
 def _null(null_block_id) -> int:
@@ -207,30 +284,34 @@ def packed_delta_rule_fn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate
     `scale` defaults to head_dim ** -0.5.  `workspace` may be a contiguous uint8 CUDA
     tensor of delta_rule_workspace bytes; else it is allocated.  Returns out
     (tokens, heads, head_dim) in q's dtype."""
-    d = _delta(q, k, v, gate, beta, states, scale, a_log, dt_bias, beta_logits, out)
-    tokens, heads, dim = q.shape
     num_seqs = max(query_start_loc.numel() - 1, 0)
-    _check_vector("query_start_loc", query_start_loc, 0, (torch.int32,))
-    _check_vector("cache_indices", cache_indices, num_seqs, (torch.int32,), strided=True)
-    _check_vector("has_initial_state", has_initial_state, num_seqs, (torch.bool, torch.uint8))
-    dev = _same_device("q", q=q, k=k, v=v, gate=gate, beta=beta, states=states, a_log=a_log,
-                       dt_bias=dt_bias, query_start_loc=query_start_loc,
-                       cache_indices=cache_indices, has_initial_state=has_initial_state, out=out,
-                       workspace=workspace)
-    with torch.cuda.device(dev):
+    index = q.get_device()
+    if not (_delta_ok(q, k, v, gate, beta, states, a_log, dt_bias, out, cache_indices, num_seqs)
+            and query_start_loc.dtype is torch.int32 and query_start_loc.dim() == 1
+            and query_start_loc.is_contiguous() and has_initial_state.dtype is torch.bool
+            and has_initial_state.dim() == 1 and has_initial_state.is_contiguous()
+            and has_initial_state.numel() >= num_seqs and query_start_loc.get_device() == index
+            and has_initial_state.get_device() == index):
+        _explain_delta(q, k, v, gate, beta, states, a_log, dt_bias, out,
+                       {"query_start_loc": query_start_loc, "cache_indices": cache_indices,
+                        "has_initial_state": has_initial_state})
+    tokens, heads, dim = q.shape
+    with _on_device(index):
         if out is None:
-            out = _empty_on(stream, q.shape, q.dtype, dev)
-        _set_out(d, out)
-        d.cache_index_stride = cache_indices.stride(0) if cache_indices.numel() > 1 else 1
+            out = _empty_like(q, stream)
         need = delta_rule_workspace(tokens, num_seqs, heads, dim, q.dtype)
         if workspace is None:
-            workspace = _empty_on(stream, (need,), torch.uint8, dev) if need else None
-        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous uint8 tensor")
+            if need:
+                workspace = _empty_on(stream, (need,), torch.uint8, q.device)
+        elif (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
+              or workspace.get_device() != index):
+            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
         _check(_lib().kda_packed_delta_rule(
-            ctypes.byref(d), tokens, cache_indices.data_ptr(), has_initial_state.data_ptr(),
-            query_start_loc.data_ptr(), num_seqs, _null(null_block_id), _ptr(workspace),
-            0 if workspace is None else workspace.numel(), _stream_of(stream, dev)))
+            _delta(q, k, v, gate, beta, states, scale, a_log, dt_bias, beta_logits, out,
+                   cache_indices), tokens, cache_indices.data_ptr(),
+            has_initial_state.data_ptr(), query_start_loc.data_ptr(), num_seqs,
+            _null(null_block_id), _ptr(workspace),
+            0 if workspace is None else workspace.numel(), _raw_stream(stream, index)))
     return out
 
 
@@ -243,18 +324,17 @@ def delta_rule_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate: t
     """One decode step of the gated delta rule: row i of q, k, v, gate, beta is the
     next token of the sequence at line cache_indices[i]; arguments as for
     packed_delta_rule_fn.  Returns out (batch, heads, head_dim)."""
-    d = _delta(q, k, v, gate, beta, states, scale, a_log, dt_bias, beta_logits, out)
-    batch = q.size(0)
-    _check_vector("cache_indices", cache_indices, batch, (torch.int32,), strided=True)
-    dev = _same_device("q", q=q, k=k, v=v, gate=gate, beta=beta, states=states, a_log=a_log,
-                       dt_bias=dt_bias, cache_indices=cache_indices, out=out)
-    with torch.cuda.device(dev):
+    index, batch = q.get_device(), q.size(0) if q.dim() else 0
+    if not _delta_ok(q, k, v, gate, beta, states, a_log, dt_bias, out, cache_indices, batch):
+        _explain_delta(q, k, v, gate, beta, states, a_log, dt_bias, out,
+                       {"cache_indices": cache_indices})
+    with _on_device(index):
         if out is None:
-            out = _empty_on(stream, q.shape, q.dtype, dev)
-        _set_out(d, out)
-        d.cache_index_stride = cache_indices.stride(0) if cache_indices.numel() > 1 else 1
-        _check(_lib().kda_delta_rule_update(ctypes.byref(d), batch, cache_indices.data_ptr(),
-                                            _null(null_block_id), _stream_of(stream, dev)))
+            out = _empty_like(q, stream)
+        _check(_lib().kda_delta_rule_update(
+            _delta(q, k, v, gate, beta, states, scale, a_log, dt_bias, beta_logits, out,
+                   cache_indices), batch, cache_indices.data_ptr(), _null(null_block_id),
+            _raw_stream(stream, index)))
     return out
 
 
@@ -292,23 +372,36 @@ def gated_rmsnorm(x: torch.Tensor, gate: torch.Tensor | None, weight: torch.Tens
     head.  x, gate, out (rows, heads, head_dim) in bf16, fp16 or fp32 with unit
     channel stride; weight fp32 (head_dim) or None.  `activation` "sigmoid" or
     "silu" ("swish"); gate None: no gate.  `out` may be x or gate."""
-    if x.dim() != 3 or x.dtype not in _DTYPES:
-        raise ValueError("x must be (rows, heads, head_dim) in bf16, fp16 or fp32")
     act = _norm_gate(gate, activation)
-    for name, t in (("x", x), ("gate", gate), ("out", out)):
-        _like(name, t, x, (x.dtype,))
-    _written("out", out)
-    rows, heads, dim = x.shape
-    _vector32("weight", weight, [(dim,)])
-    dev = _same_device("x", x=x, gate=gate, weight=weight, out=out)
-    with torch.cuda.device(dev):
+    shape, dt, index = x.shape, x.dtype, x.get_device()
+    if not (len(shape) == 3 and index >= 0 and dt in _DTYPES and x.stride(2) == 1
+            and (gate is None or (gate.dtype is dt and gate.shape == shape
+                                  and gate.stride(2) == 1 and gate.get_device() == index))
+            and (weight is None or (weight.dtype is torch.float32 and weight.shape == shape[2:]
+                                    and weight.is_contiguous() and weight.get_device() == index))
+            and (out is None or (out.dtype is dt and out.shape == shape and out.is_contiguous()
+                                 and out.get_device() == index))):
+        if x.dim() != 3 or x.dtype not in _DTYPES:
+            raise ValueError("x must be (rows, heads, head_dim) in bf16, fp16 or fp32")
+        for name, t in (("x", x), ("gate", gate), ("out", out)):
+            _like(name, t, x, (x.dtype,))
+        _written("out", out)
+        _vector32("weight", weight, [(x.size(2),)])
+        _same_device("x", x=x, gate=gate, weight=weight, out=out)
+    with _on_device(index):
         if out is None:
-            out = _empty_on(stream, x.shape, x.dtype, dev)
+            out = _empty_like(x, stream)
+        g = x if gate is None else gate
+        pairs = _SixLong(*x.stride()[:2], *g.stride()[:2], *out.stride()[:2])
+        if shape[0] <= 1:  # the stride of an axis of one entry is never used
+            pairs[0] = pairs[2] = pairs[4] = 0
+        if shape[1] == 1:
+            pairs[1] = pairs[3] = pairs[5] = 0
+        at = ctypes.addressof(pairs)
         _check(_lib().kda_gated_rmsnorm(
-            _ptr(x), _Pair(*_strides(x, 2)), _ptr(gate),
-            None if gate is None else _Pair(*_strides(gate, 2)), _ptr(weight), eps, act, rows,
-            heads, dim, _DTYPES[x.dtype], _ptr(out), _Pair(*_strides(out, 2)),
-            _stream_of(stream, dev)))
+            x.data_ptr(), at, None if gate is None else gate.data_ptr(), at + 16, _ptr(weight),
+            eps, act, shape[0], shape[1], shape[2], _DTYPES[dt], out.data_ptr(), at + 32,
+            _raw_stream(stream, index)))
     return out
 
 
@@ -323,31 +416,48 @@ def residual_rmsnorm(y: torch.Tensor, residual: torch.Tensor, weight: torch.Tens
     fp32; residual in y's dtype or fp32; weights fp32 (width).  Returns (out,
     residual_out); residual_out defaults to `residual` itself (updated in
     place).  The norm is taken of r before its rounding."""
-    if y.dim() != 2 or y.dtype not in _DTYPES:
-        raise ValueError("y must be (rows, width) in bf16, fp16 or fp32")
     act = _norm_gate(gate, activation)
-    for name, t in (("y", y), ("gate", gate), ("out", out)):
-        _like(name, t, y, (y.dtype,))
-    _like("residual", residual, y, (y.dtype, torch.float32))
-    _like("residual_out", residual_out, y, (residual.dtype,))
-    _written("out", out)
-    _written("residual_out", residual if residual_out is None else residual_out)
-    rows, width = y.shape
-    _vector32("weight", weight, [(width,)])
-    _vector32("post_weight", post_weight, [(width,)])
-    dev = _same_device("y", y=y, residual=residual, gate=gate, weight=weight,
-                       post_weight=post_weight, out=out, residual_out=residual_out)
-    with torch.cuda.device(dev):
+    shape, dt, index, rt = y.shape, y.dtype, y.get_device(), residual.dtype
+    if not (len(shape) == 2 and index >= 0 and dt in _DTYPES and y.stride(1) == 1
+            and residual.shape == shape and (rt is dt or rt is torch.float32)
+            and residual.stride(1) == 1 and residual.stride(0) > 0
+            and residual.get_device() == index
+            and (gate is None or (gate.dtype is dt and gate.shape == shape
+                                  and gate.stride(1) == 1 and gate.get_device() == index))
+            and (weight is None or (weight.dtype is torch.float32 and weight.shape == shape[1:]
+                                    and weight.is_contiguous() and weight.get_device() == index))
+            and (post_weight is None or (
+                post_weight.dtype is torch.float32 and post_weight.shape == shape[1:]
+                and post_weight.is_contiguous() and post_weight.get_device() == index))
+            and (out is None or (out.dtype is dt and out.shape == shape and out.is_contiguous()
+                                 and out.get_device() == index))
+            and (residual_out is None or (
+                residual_out.dtype is rt and residual_out.shape == shape
+                and residual_out.is_contiguous() and residual_out.get_device() == index))):
+        if y.dim() != 2 or y.dtype not in _DTYPES:
+            raise ValueError("y must be (rows, width) in bf16, fp16 or fp32")
+        for name, t in (("y", y), ("gate", gate), ("out", out)):
+            _like(name, t, y, (y.dtype,))
+        _like("residual", residual, y, (y.dtype, torch.float32))
+        _like("residual_out", residual_out, y, (residual.dtype,))
+        _written("out", out)
+        _written("residual_out", residual if residual_out is None else residual_out)
+        _vector32("weight", weight, [(y.size(1),)])
+        _vector32("post_weight", post_weight, [(y.size(1),)])
+        _same_device("y", y=y, residual=residual, gate=gate, weight=weight,
+                     post_weight=post_weight, out=out, residual_out=residual_out)
+    rows, width = shape
+    many = rows > 1  # the stride of an axis of one entry is never used
+    with _on_device(index):
         if out is None:
-            out = _empty_on(stream, y.shape, y.dtype, dev)
+            out = _empty_like(y, stream)
         if residual_out is None:
             residual_out = residual
-        stride = {n: _strides(t, 1)[0] if t is not None else 0
-                  for n, t in (("y", y), ("r", residual), ("g", gate), ("o", out),
-                               ("ro", residual_out))}
         _check(_lib().kda_residual_rmsnorm(
-            _ptr(y), stride["y"], _ptr(residual), stride["r"], _ptr(gate), stride["g"],
-            _ptr(weight), _ptr(post_weight), scale, eps, act, rows, width, _DTYPES[y.dtype],
-            int(residual.dtype == torch.float32), _ptr(out), stride["o"], _ptr(residual_out),
-            stride["ro"], _stream_of(stream, dev)))
+            y.data_ptr(), y.stride(0) if many else 0, residual.data_ptr(),
+            residual.stride(0) if many else 0, _ptr(gate),
+            gate.stride(0) if many and gate is not None else 0, _ptr(weight), _ptr(post_weight),
+            scale, eps, act, rows, width, _DTYPES[dt], 1 if rt is torch.float32 else 0,
+            out.data_ptr(), out.stride(0) if many else 0, residual_out.data_ptr(),
+            residual_out.stride(0) if many else 0, _raw_stream(stream, index)))
     return out, residual_out

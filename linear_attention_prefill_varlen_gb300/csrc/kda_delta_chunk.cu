@@ -1599,7 +1599,8 @@ static_assert(2 * (sizeof(PrepSmem<128>) + 1024) <= 228 * 1024, "two blocks of t
 template <typename T, int D, bool kChannelGate, typename G>
 cudaError_t launch_prepare(const DeltaParams &p, const ChunkPlan &plan, const WalkArgs &w, kda_stream_t stream) {
     auto *kernel = delta_prepare_kernel<T, D, kChannelGate, G>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(PrepSmem<D>));
+    static std::atomic<uint64_t> done;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), (int)sizeof(PrepSmem<D>), done);
     if (e != cudaSuccess) return e;
     // Two blocks per SM run at a time, a token chunk's heads next to each other.
     const int ahead = (int)(2 * current_sms() / p.heads) * kChunk;
@@ -1611,12 +1612,15 @@ cudaError_t launch_walk(const DeltaParams &p, const WalkArgs &w, int64_t items, 
     auto *kernel = delta_walk_kernel<T, D, kMode>;
     constexpr size_t smem = sizeof(WalkSmem<D, kMode>) + 1024;
     static_assert(smem <= 232448, "227 KB per block");
-    cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
-    if (e != cudaSuccess) return e;
-    // The roles' shares add up to exactly this; with fewer they would wait for registers for ever.
-    if (attr.numRegs != Regs<kMode>::launch) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done;
+    if (done.load(std::memory_order_relaxed) == 0) {
+        // The roles' shares add up to exactly this; with fewer they would wait for registers for ever.
+        cudaFuncAttributes attr;
+        const cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs != Regs<kMode>::launch) return cudaErrorInvalidConfiguration;
+    }
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), (int)smem, done);
     if (e != cudaSuccess) return e;
     const int64_t blocks = items < current_sms() ? items : current_sms();
     return launch(kernel, dim3((unsigned)blocks), kWalkThreads<kMode>, smem, stream, p, w);
@@ -1644,7 +1648,8 @@ cudaError_t run(const DeltaParams &p, const kda_delta_t *d, const ChunkPlan &pla
         e = launch_walk<T, D, kWalkSummary>(p, w, marks * p.heads, stream);
         if (e != cudaSuccess) return e;
         auto *join = delta_join_kernel<D>;
-        e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(JoinSmem<D>));
+        static std::atomic<uint64_t> done;
+        e = allow_smem(reinterpret_cast<const void *>(join), (int)sizeof(JoinSmem<D>), done);
         if (e != cudaSuccess) return e;
         e = launch(join, dim3((unsigned)marks, (unsigned)p.heads, D / kJoinRows), kJoinThreads, sizeof(JoinSmem<D>),
                    stream, p, w);

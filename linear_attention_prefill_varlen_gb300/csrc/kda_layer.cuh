@@ -48,6 +48,41 @@ __device__ __forceinline__ void st_vec(T *p, const Vec<T, N> &x) {
     *reinterpret_cast<Vec<T, N> *>(p) = x;
 }
 
+// The same 16 bytes without keeping them in L1: read once.
+template <typename T, int N>
+__device__ __forceinline__ Vec<T, N> ld_stream(const T *p) {
+    static_assert(sizeof(Vec<T, N>) == 16, "16-byte vectors");
+    Vec<T, N> x;
+    uint4 &u = *reinterpret_cast<uint4 *>(&x);
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p) : "memory");
+    return x;
+}
+
+// Division by a divisor fixed for a launch: for 1 <= d < 2^31, l = ceil(log2 d)
+// and m = floor(2^32 (2^l - d) / d) + 1, every n < 2^32 has n / d =
+// (t + ((n - t) >> min(l, 1))) >> max(l - 1, 0) with t = umulhi(m, n) (Granlund and
+// Montgomery, 1994).
+struct FastDiv {
+    uint32_t m;
+    int s1, s2;
+};
+
+inline FastDiv make_fast_div(uint32_t d) {
+    int l = 0;
+    while ((uint64_t(1) << l) < d) ++l;
+    FastDiv f;
+    f.m = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << l) - d)) / d + 1);
+    f.s1 = l < 1 ? l : 1;
+    f.s2 = l > 1 ? l - 1 : 0;
+    return f;
+}
+
+__device__ __forceinline__ uint32_t fast_div(uint32_t n, FastDiv f) {
+    const uint32_t t = __umulhi(f.m, n);
+    return (t + ((n - t) >> f.s1)) >> f.s2;
+}
+
 // One element of a tensor whose type is known at run time (beta, per-head gates).
 __device__ __forceinline__ float ld_dyn(const void *p, int64_t i, int dtype) {
     if (dtype == KDA_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
@@ -75,6 +110,19 @@ inline bool dtype_ok(int dtype) { return dtype >= KDA_DTYPE_BF16 && dtype <= KDA
 char *error_buffer();  // the calling thread's text (256 bytes), kda_norm.cu
 kda_status_t cuda_status(cudaError_t e);
 int current_sms();
+
+// Lets a kernel take `bytes` of dynamic shared memory, once per device (`done`: a bit
+// each; threads that race set the same value).
+inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // A launch as programmatic dependent of the preceding kernel (dependency_wait).
 template <typename... Args>

@@ -33,10 +33,21 @@ int current_sms() {
 
 namespace {
 
-template <int kAct>
+// The gate's factor. For a 16-bit gate the exponential and the reciprocal are the
+// special-function unit's (relative error 2^-23 times the argument, below 2^-16
+// where the factor is above e^-80): the accurate forms cost more issue slots than
+// the loads and stores leave.
+template <typename T, int kAct>
 __device__ __forceinline__ float act_f(float z) {
     if constexpr (kAct == KDA_NORM_GATE_NONE) return 1.0f;
-    const float s = sigmoid_f(z);
+    float s;
+    if constexpr (sizeof(T) == 2) {
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    } else {
+        s = sigmoid_f(z);
+    }
     return kAct == KDA_NORM_GATE_SILU ? z * s : s;
 }
 
@@ -47,75 +58,95 @@ struct GatedParams {
     int64_t xs[2], gs[2], os[2];
     int64_t groups;  // rows * heads
     int heads;
+    FastDiv heads_div;
     int vecs;  // 16-byte vectors per head
     float eps, inv_dim;
 };
 
 // kLanes neighbouring lanes own one (row, head); each holds kVpl vectors of it
-// in registers, so x is read once and the sum of squares is a butterfly.
-template <typename T, int kLanes, int kVpl, int kAct>
-__global__ void __launch_bounds__(256) gated_rmsnorm_kernel(GatedParams p) {
-    constexpr int N = 16 / sizeof(T);
+// in registers, so x is read once and the sum of squares is a butterfly. A block
+// takes kBatch times as many heads as it has groups of lanes, a block's width
+// apart, with all their loads issued first: one head's two loads per thread leave
+// too few bytes in flight.
+template <typename T, int kLanes, int kVpl, int kBatch, int kAct>
+__global__ void __launch_bounds__(256) gated_rmsnorm_kernel(const __grid_constant__ GatedParams p) {
+    constexpr int N = 16 / sizeof(T), kPerBlock = 256 / kLanes;
     dependency_wait();
-    const int64_t group = (int64_t(blockIdx.x) * 256 + threadIdx.x) / kLanes;
     const int lane = threadIdx.x % kLanes;
-    const bool live = group < p.groups;
-    const int64_t row = live ? group / p.heads : 0, head = live ? group % p.heads : 0;
-    const T *x = static_cast<const T *>(p.x) + row * p.xs[0] + head * p.xs[1];
-    const T *gate = static_cast<const T *>(p.gate) + row * p.gs[0] + head * p.gs[1];
-    T *out = static_cast<T *>(p.out) + row * p.os[0] + head * p.os[1];
-    Vec<T, N> xv[kVpl], gv[kVpl];
+    const int64_t first = (int64_t)blockIdx.x * (kPerBlock * kBatch) + threadIdx.x / kLanes;
+    Vec<T, N> xv[kBatch][kVpl], gv[kBatch][kVpl];
+    auto at_of = [&](int b, const int64_t *s) {
+        const int64_t group = min(first + b * kPerBlock, p.groups - 1);
+        const int64_t row = fast_div((uint32_t)group, p.heads_div), head = group - row * p.heads;
+        return row * s[0] + head * s[1];
+    };
 #pragma unroll
-    for (int i = 0; i < kVpl; ++i) {
-        const int at = lane + i * kLanes;
-        if (live && at < p.vecs) {
-            xv[i] = ld_vec<T, N>(x + at * N);
-            if constexpr (kAct != KDA_NORM_GATE_NONE) gv[i] = ld_vec<T, N>(gate + at * N);
-        } else {
+    for (int b = 0; b < kBatch; ++b) {
+        const T *x = static_cast<const T *>(p.x) + at_of(b, p.xs);
+        const T *gate = static_cast<const T *>(p.gate) + at_of(b, p.gs);
 #pragma unroll
-            for (int j = 0; j < N; ++j) xv[i].v[j] = gv[i].v[j] = from_f<T>(0.0f);
+        for (int i = 0; i < kVpl; ++i) {
+            const int at = min(lane + i * kLanes, p.vecs - 1);
+            xv[b][i] = ld_stream<T, N>(x + at * N);
+            if constexpr (kAct != KDA_NORM_GATE_NONE) gv[b][i] = ld_stream<T, N>(gate + at * N);
         }
     }
-    float sum = 0.0f;
+    float w[kVpl][N];
 #pragma unroll
     for (int i = 0; i < kVpl; ++i)
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float f = to_f<T>(xv[i].v[j]);
-            sum = fmaf(f, f, sum);
-        }
-#pragma unroll
-    for (int m = kLanes / 2; m > 0; m /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    const float inv = rsqrtf(fmaf(sum, p.inv_dim, p.eps));
-#pragma unroll
-    for (int i = 0; i < kVpl; ++i) {
-        const int at = lane + i * kLanes;
-        if (!live || at >= p.vecs) continue;
-        float w[N];
 #pragma unroll
         for (int j = 0; j < N; j += 4) {
             float4 f = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
             if (p.weight != nullptr)
-                f = __ldg(reinterpret_cast<const float4 *>(p.weight + at * N + j));
-            w[j] = f.x, w[j + 1] = f.y, w[j + 2] = f.z, w[j + 3] = f.w;
+                f = __ldg(reinterpret_cast<const float4 *>(p.weight + min(lane + i * kLanes, p.vecs - 1) * N + j));
+            w[i][j] = f.x, w[i][j + 1] = f.y, w[i][j + 2] = f.z, w[i][j + 3] = f.w;
         }
-        Vec<T, N> y;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            y.v[j] = from_f<T>(to_f<T>(xv[i].v[j]) * inv * w[j] * act_f<kAct>(to_f<T>(gv[i].v[j])));
-        st_vec<T, N>(out + at * N, y);
+    for (int b = 0; b < kBatch; ++b) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kVpl; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float f = to_f<T>(xv[b][i].v[j]);
+                if (lane + i * kLanes < p.vecs) sum = fmaf(f, f, sum);
+            }
+#pragma unroll
+        for (int m = kLanes / 2; m > 0; m /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        const float inv = rsqrtf(fmaf(sum, p.inv_dim, p.eps));
+        if (first + b * kPerBlock >= p.groups) continue;
+        T *out = static_cast<T *>(p.out) + at_of(b, p.os);
+#pragma unroll
+        for (int i = 0; i < kVpl; ++i) {
+            const int at = lane + i * kLanes;
+            if (at >= p.vecs) continue;
+            Vec<T, N> y;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                y.v[j] = from_f<T>(to_f<T>(xv[b][i].v[j]) * inv * w[i][j] * act_f<T, kAct>(to_f<T>(gv[b][i].v[j])));
+            st_vec<T, N>(out + at * N, y);
+        }
     }
+}
+
+template <typename T, int kLanes, int kVpl, int kBatch>
+cudaError_t launch_gated_batch(const GatedParams &p, int act, kda_stream_t stream) {
+    constexpr int kHeads = 256 / kLanes * kBatch;
+    const dim3 grid((unsigned)((p.groups + kHeads - 1) / kHeads));
+    if (act == KDA_NORM_GATE_NONE)
+        return launch(gated_rmsnorm_kernel<T, kLanes, kVpl, kBatch, KDA_NORM_GATE_NONE>, grid, 256, 0, stream, p);
+    if (act == KDA_NORM_GATE_SIGMOID)
+        return launch(gated_rmsnorm_kernel<T, kLanes, kVpl, kBatch, KDA_NORM_GATE_SIGMOID>, grid, 256, 0, stream, p);
+    return launch(gated_rmsnorm_kernel<T, kLanes, kVpl, kBatch, KDA_NORM_GATE_SILU>, grid, 256, 0, stream, p);
 }
 
 template <typename T, int kLanes, int kVpl>
 cudaError_t launch_gated(const GatedParams &p, int act, kda_stream_t stream) {
-    const int64_t blocks = (p.groups * kLanes + 255) / 256;
-    const dim3 grid((unsigned)blocks);
-    if (act == KDA_NORM_GATE_NONE)
-        return launch(gated_rmsnorm_kernel<T, kLanes, kVpl, KDA_NORM_GATE_NONE>, grid, 256, 0, stream, p);
-    if (act == KDA_NORM_GATE_SIGMOID)
-        return launch(gated_rmsnorm_kernel<T, kLanes, kVpl, KDA_NORM_GATE_SIGMOID>, grid, 256, 0, stream, p);
-    return launch(gated_rmsnorm_kernel<T, kLanes, kVpl, KDA_NORM_GATE_SILU>, grid, 256, 0, stream, p);
+    // Batches only where they still leave every SM several blocks.
+    if constexpr (kVpl == 1)
+        if (p.groups * kLanes >= (int64_t)256 * 4 * 8 * current_sms())
+            return launch_gated_batch<T, kLanes, kVpl, 4>(p, act, stream);
+    return launch_gated_batch<T, kLanes, kVpl, 1>(p, act, stream);
 }
 
 template <typename T>
@@ -151,49 +182,78 @@ __device__ __forceinline__ float block_sum(float v, float *slot, int warps) {
     return s;
 }
 
-// One block per row at a time; a thread owns kVpt vectors of the row, keeps y
-// and then r in registers between the reductions.
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+
+// 16-byte pieces a thread holds of one row.
+template <typename T, typename R, int kVpt, bool kGate>
+constexpr int kPieces = kVpt * (1 + (kGate ? 1 : 0) + (int)(sizeof(R) / sizeof(T)));
+template <int kVpt>
+constexpr int kRowsAhead = kVpt < 4 ? 2 : 1;  // the widest rows' pieces fill 128 KB
+
+// A block takes rows blockIdx.x, + gridDim.x, ...; a thread owns kVpt vectors of a
+// row, keeps y and then r in registers between the reductions, and has its pieces
+// of the next kRowsAhead rows on their way into its own part of shared memory (it
+// alone reads them, so no barrier guards them): held in registers they would leave
+// too few threads on the SM to keep HBM busy.
 template <typename T, typename R, int kVpt, int kAct, bool kPost>
-__global__ void __launch_bounds__(512) residual_rmsnorm_kernel(ResidualParams p) {
-    constexpr int N = 16 / sizeof(T);
-    constexpr int NR = N * sizeof(R) / 16;   // 16-byte loads of a residual vector
-    constexpr int RE = 16 / sizeof(R);
+__global__ void __launch_bounds__(512) residual_rmsnorm_kernel(const __grid_constant__ ResidualParams p) {
+    constexpr bool kGate = kAct != KDA_NORM_GATE_NONE;
+    constexpr int N = 16 / sizeof(T), NR = sizeof(R) / sizeof(T), RE = 16 / sizeof(R);
+    constexpr int kAll = kPieces<T, R, kVpt, kGate>;
     __shared__ float slots[2][32];
+    extern __shared__ uint4 ring[];  // [row ahead][piece][thread]
     dependency_wait();
     const int warps = blockDim.x / 32;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const T *y = static_cast<const T *>(p.y) + row * p.ys;
-        const T *gate = static_cast<const T *>(p.gate) + row * p.gs;
-        const R *res = static_cast<const R *>(p.residual) + row * p.rs;
+    auto fetch = [&](int64_t row, int slot) {
+        if (row < p.rows) {
+            uint4 *to = ring + slot * kAll * blockDim.x + threadIdx.x;
+#pragma unroll
+            for (int i = 0; i < kVpt; ++i) {
+                const int at = threadIdx.x + i * blockDim.x;
+                if (at >= p.vecs) continue;
+                copy16(to + i * blockDim.x, static_cast<const T *>(p.y) + row * p.ys + at * N);
+                if constexpr (kGate)
+                    copy16(to + (kVpt + i) * blockDim.x, static_cast<const T *>(p.gate) + row * p.gs + at * N);
+#pragma unroll
+                for (int c = 0; c < NR; ++c)
+                    copy16(to + ((kGate ? 2 : 1) * kVpt + i * NR + c) * blockDim.x,
+                           static_cast<const R *>(p.residual) + row * p.rs + at * N + c * RE);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kRowsAhead<kVpt>; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+    int slot = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, slot = slot + 1 == kRowsAhead<kVpt> ? 0 : slot + 1) {
+        copies_wait<kRowsAhead<kVpt> - 1>();
+        const uint4 *from = ring + slot * kAll * blockDim.x + threadIdx.x;
         Vec<T, N> yv[kVpt], gv[kVpt];
         Vec<R, RE> rv[kVpt][NR];
 #pragma unroll
         for (int i = 0; i < kVpt; ++i) {
-            const int at = threadIdx.x + i * blockDim.x;
-            if (at < p.vecs) {
-                yv[i] = ld_vec<T, N>(y + at * N);
-                if constexpr (kAct != KDA_NORM_GATE_NONE) gv[i] = ld_vec<T, N>(gate + at * N);
+            *reinterpret_cast<uint4 *>(&yv[i]) = from[i * blockDim.x];
+            if constexpr (kGate) *reinterpret_cast<uint4 *>(&gv[i]) = from[(kVpt + i) * blockDim.x];
 #pragma unroll
-                for (int c = 0; c < NR; ++c) rv[i][c] = ld_vec<R, RE>(res + at * N + c * RE);
-            } else {
-#pragma unroll
-                for (int j = 0; j < N; ++j) yv[i].v[j] = gv[i].v[j] = from_f<T>(0.0f);
-#pragma unroll
-                for (int c = 0; c < NR; ++c)
-#pragma unroll
-                    for (int j = 0; j < RE; ++j) rv[i][c].v[j] = from_f<R>(0.0f);
-            }
+            for (int c = 0; c < NR; ++c)
+                *reinterpret_cast<uint4 *>(&rv[i][c]) = from[((kGate ? 2 : 1) * kVpt + i * NR + c) * blockDim.x];
         }
+        fetch(row + (int64_t)kRowsAhead<kVpt> * gridDim.x, slot);
         float inv_y = 1.0f;
         if constexpr (kPost) {
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kVpt; ++i)
+                if ((int)(threadIdx.x + i * blockDim.x) < p.vecs)
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const float f = to_f<T>(yv[i].v[j]);
-                    sum = fmaf(f, f, sum);
-                }
+                    for (int j = 0; j < N; ++j) {
+                        const float f = to_f<T>(yv[i].v[j]);
+                        sum = fmaf(f, f, sum);
+                    }
             inv_y = rsqrtf(fmaf(block_sum(sum, slots[0], warps), p.inv_width, p.eps));
         }
         float r[kVpt][N];
@@ -212,7 +272,7 @@ __global__ void __launch_bounds__(512) residual_rmsnorm_kernel(ResidualParams p)
                 for (int c = 0; c < 4; ++c) {
                     float b = to_f<T>(yv[i].v[j + c]);
                     if constexpr (kPost) b = b * inv_y * ws[c];
-                    if constexpr (kAct != KDA_NORM_GATE_NONE) b *= act_f<kAct>(to_f<T>(gv[i].v[j + c]));
+                    if constexpr (kGate) b *= act_f<T, kAct>(to_f<T>(gv[i].v[j + c]));
                     const float f = fmaf(p.scale, b, to_f<R>(rv[i][(j + c) / RE].v[(j + c) % RE]));
                     r[i][j + c] = in ? f : 0.0f;
                     sum = fmaf(r[i][j + c], r[i][j + c], sum);
@@ -257,13 +317,26 @@ __global__ void __launch_bounds__(512) residual_rmsnorm_kernel(ResidualParams p)
     }
 }
 
+template <typename T, typename R, int kVpt, int kAct, bool kPost>
+cudaError_t launch_residual_post(const ResidualParams &p, kda_stream_t stream) {
+    const unsigned threads = (unsigned)(((p.vecs + kVpt - 1) / kVpt + 31) / 32 * 32);
+    auto *kernel = residual_rmsnorm_kernel<T, R, kVpt, kAct, kPost>;
+    const size_t smem = (size_t)threads * 16 * kRowsAhead<kVpt> * kPieces<T, R, kVpt, kAct != KDA_NORM_GATE_NONE>;
+    static std::atomic<uint64_t> done;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), 512 * 16 * kRowsAhead<kVpt> *
+                                     kPieces<T, R, kVpt, kAct != KDA_NORM_GATE_NONE>, done);
+    if (e != cudaSuccess) return e;
+    // About as many blocks as are resident; they loop over the rows.
+    const int64_t fit = 1536 / threads, room = (int64_t)(220 * 1024 / smem);
+    const int64_t most = current_sms() * (fit < 1 || room < 1 ? 1 : fit < room ? fit : room);
+    const int64_t blocks = p.rows < most ? p.rows : most;
+    return launch(kernel, dim3((unsigned)blocks), threads, smem, stream, p);
+}
+
 template <typename T, typename R, int kVpt, int kAct>
 cudaError_t launch_residual(const ResidualParams &p, kda_stream_t stream) {
-    const unsigned threads = (unsigned)(((p.vecs + kVpt - 1) / kVpt + 31) / 32 * 32);
-    const dim3 grid((unsigned)(p.rows < (int64_t(1) << 30) ? p.rows : (int64_t(1) << 30)));
-    if (p.post != nullptr)
-        return launch(residual_rmsnorm_kernel<T, R, kVpt, kAct, true>, grid, threads, 0, stream, p);
-    return launch(residual_rmsnorm_kernel<T, R, kVpt, kAct, false>, grid, threads, 0, stream, p);
+    return p.post != nullptr ? launch_residual_post<T, R, kVpt, kAct, true>(p, stream)
+                             : launch_residual_post<T, R, kVpt, kAct, false>(p, stream);
 }
 
 template <typename T, typename R, int kVpt>
@@ -313,7 +386,7 @@ kda_status_t kda_gated_rmsnorm(const void *x, const int64_t x_stride[2], const v
         !norm_scalars_ok(eps, activation, rows > 0 ? gate : &eps))
         return KDA_ERR_INVALID_ARG;
     const int64_t quantum = 16 / dtype_bytes(dtype);
-    if (head_dim % quantum != 0 || head_dim > 128 * quantum || heads > INT32_MAX)
+    if (head_dim % quantum != 0 || head_dim > 128 * quantum || heads > (1 << 30))
         return KDA_ERR_UNSUPPORTED;
     if (rows == 0) return KDA_OK;
     const bool gated = activation != KDA_NORM_GATE_NONE;
@@ -332,6 +405,7 @@ kda_status_t kda_gated_rmsnorm(const void *x, const int64_t x_stride[2], const v
     }
     p.groups = rows * heads;
     p.heads = (int)heads;
+    p.heads_div = make_fast_div((uint32_t)heads);
     p.vecs = (int)(head_dim / quantum);
     p.eps = eps;
     p.inv_dim = 1.0f / (float)head_dim;
