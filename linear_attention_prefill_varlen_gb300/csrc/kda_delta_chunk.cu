@@ -268,21 +268,6 @@ __device__ __forceinline__ void store_split(__half *hi, __half *lo, const float2
     }
 }
 
-// The sums over the warp of 16 values, value i to lanes 2 i and 2 i + 1.
-__device__ __forceinline__ float scatter_sum(float (&v)[16], int lane) {
-#pragma unroll
-    for (int m = 16; m > 1; m /= 2) {
-        const bool up = lane & m;
-#pragma unroll
-        for (int i = 0; i < m / 2; ++i) {
-            const float send = up ? v[i] : v[i + m / 2];
-            const float keep = up ? v[i + m / 2] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-        }
-    }
-    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
-}
-
 // Keeps the compiler from carrying the FP32 forms of packed halves from one stage
 // to the next, which would not fit in the registers.
 template <typename X>
