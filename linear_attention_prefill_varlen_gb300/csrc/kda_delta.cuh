@@ -43,14 +43,6 @@ __device__ __forceinline__ float softplus_f(float x) {
     return fmaf(c, e, fmaxf(x, 0.0f));
 }
 
-// top + log1p(e) of two values.
-__device__ __forceinline__ float2 softplus_tail2(float2 e, float2 top) {
-    float2 c = make_float2(kLog1p[9], kLog1p[9]);
-#pragma unroll
-    for (int i = 8; i >= 0; --i) c = __ffma2_rn(c, e, make_float2(kLog1p[i], kLog1p[i]));
-    return __ffma2_rn(c, e, top);
-}
-
 // What decay_of multiplies: -exp(a_log) log2(e), or log2(e) for a log gate.
 __device__ __forceinline__ float gate_factor(const float *a_log, int h, int kind) {
     return kind == KDA_GATE_SOFTPLUS ? -expf(a_log[h]) * 1.4426950408889634f : 1.4426950408889634f;

@@ -228,18 +228,6 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-// decay_of for two channels.
-__device__ __forceinline__ float2 decay2_of(float2 raw, int kind, float factor, float2 bias) {
-    float2 x = raw;
-    if (kind == KDA_GATE_SOFTPLUS) {
-        x = __fadd2_rn(raw, bias);
-        const float2 e = make_float2(exp2_f(fabsf(x.x) * -1.4426950408889634f), exp2_f(fabsf(x.y) * -1.4426950408889634f));
-        x = softplus_tail2(e, make_float2(fmaxf(x.x, 0.0f), fmaxf(x.y, 0.0f)));
-    }
-    x = mul2(x, make_float2(factor, factor));
-    return make_float2(exp2_f(x.x), exp2_f(x.y));
-}
-
 __device__ __forceinline__ void split2(float2 f, uint32_t &hi, uint32_t &lo) {
     const __half2 h = __float22half2_rn(f);
     const float2 g = __half22float2(h);
@@ -400,16 +388,27 @@ __global__ void __launch_bounds__(256, 2)
         for (int c = 0; c < P; ++c) whole[c] = make_float2(1.0f, 1.0f);
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            const bool in = b * 8 + r < n;
-            const float same = kChannelGate || !in ? 1.0f : decay_of(one[r], p.gate_kind, factor, bias[0]);
+            const float same = kChannelGate ? 1.0f : decay_of(one[r], p.gate_kind, factor, bias[0]);
 #pragma unroll
             for (int c = 0; c < P; ++c) {
                 a[r][c] = make_float2(same, same);
                 if constexpr (kChannelGate) {
-                    a[r][c] = decay2_of(make_float2(to_f<G>(gv[r].v[2 * c]), to_f<G>(gv[r].v[2 * c + 1])), p.gate_kind,
-                                        factor, make_float2(bias[2 * c], bias[2 * c + 1]));
-                    if (!in) a[r][c] = make_float2(1.0f, 1.0f);
+                    a[r][c] = make_float2(decay_of(to_f<G>(gv[r].v[2 * c]), p.gate_kind, factor, bias[2 * c]),
+                                          decay_of(to_f<G>(gv[r].v[2 * c + 1]), p.gate_kind, factor, bias[2 * c + 1]));
                 }
+            }
+        }
+        if (b * 8 + 8 > n) {  // rows past the end
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (b * 8 + r >= n)
+#pragma unroll
+                    for (int c = 0; c < P; ++c) a[r][c] = make_float2(1.0f, 1.0f);
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+#pragma unroll
+            for (int c = 0; c < P; ++c) {
                 whole[c] = mul2(whole[c], a[r][c]);
             }
         }
@@ -442,9 +441,9 @@ __global__ void __launch_bounds__(256, 2)
             float2 f[P];
 #pragma unroll
             for (int c = 0; c < P; ++c) {
-                k[r][c] = __floats2half2_rn(to_f<T>(kv[r].v[2 * c]) * up_k, to_f<T>(kv[r].v[2 * c + 1]) * up_k);
-                q[r][c] = __floats2half2_rn(to_f<T>(qv[r].v[2 * c]) * up_q, to_f<T>(qv[r].v[2 * c + 1]) * up_q);
-                f[c] = make_float2(to_f<T>(vv[r].v[2 * c]) * up_v, to_f<T>(vv[r].v[2 * c + 1]) * up_v);
+                k[r][c] = __float22half2_rn(mul2(make_float2(to_f<T>(kv[r].v[2 * c]), to_f<T>(kv[r].v[2 * c + 1])), make_float2(up_k, up_k)));
+                q[r][c] = __float22half2_rn(mul2(make_float2(to_f<T>(qv[r].v[2 * c]), to_f<T>(qv[r].v[2 * c + 1])), make_float2(up_q, up_q)));
+                f[c] = mul2(make_float2(to_f<T>(vv[r].v[2 * c]), to_f<T>(vv[r].v[2 * c + 1])), make_float2(up_v, up_v));
             }
             store_row<P>(&sm.l.v[b * 8 + r][lane * C], f);
         }
@@ -453,39 +452,40 @@ __global__ void __launch_bounds__(256, 2)
     constexpr float kDownA = 0x1p-22f;
     const float down_kk = down_k * down_k;
 
-    // ---- pairs inside 8 tokens: running products of decays, FP32. For j = 0..7:
-    // q_j k_j, then for i > j the pair (k_i k_j, q_i k_j); 64 sums in batches of 16.
+    // ---- pairs inside 8 tokens: running products of decays, FP32. For i = 0..7: q_i k_i,
+    // then for j < i the pair (k_i k_j, q_i k_j); 64 sums in batches of 16.
     {
         repack(k), repack(q);
         float f[16];
+        float2 w[8][P];  // k_j decayed to token i
 #pragma unroll
-        for (int jj = 0; jj < 8; ++jj) {
-            const int first = jj * (16 - jj);
-            float2 w[P];
+        for (int ii = 0; ii < 8; ++ii) {
+            float2 ki[P], qi[P];
 #pragma unroll
-            for (int ii = jj; ii < 8; ++ii) {
-                float2 sk = make_float2(0.0f, 0.0f), sq = sk;
+            for (int c = 0; c < P; ++c) {
+                ki[c] = __half22float2(k[ii][c]), qi[c] = __half22float2(q[ii][c]);
+                w[ii][c] = ki[c];
+            }
+#pragma unroll
+            for (int e = 0; e <= 2 * ii; ++e) {  // 0: q_i k_i, 1 + 2 j: k_i k_j, 2 + 2 j: q_i k_j
+                const int jj = e == 0 ? ii : (e - 1) / 2;
+                const bool of_k = e % 2 == 1;
+                float2 sum;
 #pragma unroll
                 for (int c = 0; c < P; ++c) {
-                    w[c] = ii == jj ? __half22float2(k[jj][c]) : mul2(w[c], a[ii][c]);
-                    const float2 ki = __half22float2(k[ii][c]), qi = __half22float2(q[ii][c]);
-                    if (ii > jj) sk = c == 0 ? mul2(ki, w[c]) : fma2(ki, w[c], sk);
-                    sq = c == 0 ? mul2(qi, w[c]) : fma2(qi, w[c], sq);
+                    if (of_k) w[jj][c] = mul2(w[jj][c], a[ii][c]);
+                    const float2 x = of_k ? ki[c] : qi[c];
+                    sum = c == 0 ? mul2(x, w[jj][c]) : fma2(x, w[jj][c], sum);
                 }
-#pragma unroll
-                for (int what = 0; what < 2; ++what) {
-                    if (ii == jj && what == 0) continue;
-                    const int at = first + 2 * (ii - jj) - 1 + what;  // 2 (i - j) - 1: k, 2 (i - j): q
-                    f[at % 16] = what ? sq.x + sq.y : sk.x + sk.y;
-                    if (at % 16 == 15) {
-                        const float got = scatter_sum(f, lane);
-                        const int mine = at - 15 + lane / 2;
-                        const int j = (mine >= 15) + (mine >= 28) + (mine >= 39) + (mine >= 48) +
-                                      (mine >= 55) + (mine >= 60) + (mine >= 63);
-                        const int e = mine - j * (16 - j), i = j + (e + 1) / 2;
-                        if (e % 2 == 1) sm.l.L[b * 8 + i][b * 8 + j] = got * down_kk * sm.beta[b * 8 + i];
-                        else sm.A[b * 8 + i][b * 8 + j] = __float2half_rn(got * kDownA);
-                    }
+                const int at = ii * ii + e;
+                f[at % 16] = sum.x + sum.y;
+                if (at % 16 == 15) {
+                    const float got = scatter_sum(f, lane);
+                    const int mine = at - 15 + lane / 2;
+                    const int i = (mine >= 1) + (mine >= 4) + (mine >= 9) + (mine >= 16) + (mine >= 25) + (mine >= 36) + (mine >= 49);
+                    const int own = mine - i * i, j = own == 0 ? i : (own - 1) / 2;
+                    if (own % 2 == 1) sm.l.L[b * 8 + i][b * 8 + j] = got * down_kk * sm.beta[b * 8 + i];
+                    else sm.A[b * 8 + i][b * 8 + j] = __float2half_rn(got * kDownA);
                 }
             }
         }
@@ -494,6 +494,8 @@ __global__ void __launch_bounds__(256, 2)
     // ---- pairs of blocks: per level, the later half's tokens carry the decays
     // from the middle to them, the earlier half's those from them to the middle
     const int g = lane / 4, cc = lane % 4 * 2;
+    constexpr int kRow = PrepSmem<D>::kRow, kPlane = 32 * kRow * 2;  // bytes from hi to lo
+    const uint32_t at_lk = smem_u32(sm.x.lv.lk_hi), at_lq = smem_u32(sm.x.lv.lq), at_rk = smem_u32(sm.x.lv.rk_hi);
 #pragma unroll 1
     for (int half = 1; half <= 4; half *= 2) {  // blocks of 8 in half a level: 1, 2, 4
         repack(k), repack(q);
@@ -535,16 +537,16 @@ __global__ void __launch_bounds__(256, 2)
             if (b < 4) {  // pair b: rows of k in the tile's first 8 rows, of q in the others
                 float c[4] = {}, c1[4] = {}, c2[4] = {};
                 const int lr = lane % 8, piece = lane / 8;
-                const __half *top = (piece & 1) ? sm.x.lv.lq[b * 8 + lr] : sm.x.lv.lk_hi[b * 8 + lr];
-                const __half *low = sm.x.lv.lk_lo[b * 8 + lr];
-                const int br = b * 8 + lane % 8, bk = (lane / 8 % 2) * 8;
+                const uint32_t left = (uint32_t)((b * 8 + lr) * kRow + (piece >> 1) * 8) * 2;
+                const uint32_t top = left + ((piece & 1) ? at_lq : at_lk), low = left + at_lk + kPlane;
+                const uint32_t right = at_rk + (uint32_t)((b * 8 + lane % 8) * kRow + (lane / 8 % 2) * 8) * 2;
 #pragma unroll
                 for (int kk = 0; kk < D; kk += 16) {
                     uint32_t ah[4], al[4], bh[2], bl[2];
-                    ldsm4(ah, smem_u32(top + kk + (piece >> 1) * 8));
-                    ldsm4(al, smem_u32(low + kk + (piece >> 1) * 8));
-                    ldsm2(bh, smem_u32(&sm.x.lv.rk_hi[br][kk + bk]));
-                    ldsm2(bl, smem_u32(&sm.x.lv.rk_lo[br][kk + bk]));
+                    ldsm4(ah, top + kk * 2);
+                    ldsm4(al, low + kk * 2);
+                    ldsm2(bh, right + kk * 2);
+                    ldsm2(bl, right + kPlane + kk * 2);
                     al[1] = al[3] = 0;
                     mma16(c, ah, bh);
                     mma16(c1, al, bh);
@@ -565,23 +567,23 @@ __global__ void __launch_bounds__(256, 2)
             const int nt = wide ? b % 4 : m * 2 + b / 2 % 2;  // 8-row tile of the right operand
             const bool do_k = wide || b % 2 == 0, do_q = wide || b % 2 == 1;
             float ck[4] = {}, ck1[4] = {}, ck2[4] = {}, cq[4] = {};
-            const int ar = m * 16 + lane % 16, ak = lane / 16 * 8;
-            const int br = nt * 8 + lane % 8, bk = (lane / 8 % 2) * 8;
+            const uint32_t left = (uint32_t)((m * 16 + lane % 16) * kRow + lane / 16 * 8) * 2;
+            const uint32_t right = at_rk + (uint32_t)((nt * 8 + lane % 8) * kRow + (lane / 8 % 2) * 8) * 2;
 #pragma unroll
             for (int kk = 0; kk < D; kk += 16) {
                 uint32_t ah[4], bh[2];
-                ldsm2(bh, smem_u32(&sm.x.lv.rk_hi[br][kk + bk]));
+                ldsm2(bh, right + kk * 2);
                 if (do_k) {
                     uint32_t al[4], bl[2];
-                    ldsm4(ah, smem_u32(&sm.x.lv.lk_hi[ar][kk + ak]));
-                    ldsm4(al, smem_u32(&sm.x.lv.lk_lo[ar][kk + ak]));
-                    ldsm2(bl, smem_u32(&sm.x.lv.rk_lo[br][kk + bk]));
+                    ldsm4(ah, at_lk + left + kk * 2);
+                    ldsm4(al, at_lk + kPlane + left + kk * 2);
+                    ldsm2(bl, right + kPlane + kk * 2);
                     mma16(ck, ah, bh);
                     mma16(ck1, al, bh);
                     mma16(ck2, ah, bl);
                 }
                 if (do_q) {
-                    ldsm4(ah, smem_u32(&sm.x.lv.lq[ar][kk + ak]));
+                    ldsm4(ah, at_lq + left + kk * 2);
                     mma16(cq, ah, bh);
                 }
             }
@@ -628,8 +630,7 @@ __global__ void __launch_bounds__(256, 2)
             for (int c = 0; c < P; ++c)
                 run[c] = mul2(run[c], *reinterpret_cast<const float2 *>(&sm.block_decay[o][lane * C + 2 * c]));
         // row 8 b + r of the image: its 16-byte piece is at piece ^ r
-        char *qo = out + Slot<D>::qw + (lane * C >> 6) * Slot<D>::kBlock + b * 8 * 128 + (lane * C & 7) * 2;
-        const int piece = lane * C >> 3 & 7;
+        const int qo = Slot<D>::qw + (lane * C >> 6) * Slot<D>::kBlock + b * 8 * 128 + (lane * C >> 3 & 7) * 16 + (lane * C & 7) * 2;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             float2 f[P], fq[P];
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(256, 2)
                 fq[c] = mul2(__half22float2(q[r][c]), run[c]);
             }
             store_split<P>(&sm.x.kg.k_hi[b * 8 + r][lane * C], &sm.x.kg.k_lo[b * 8 + r][lane * C], f);
-            store_row<P>(qo + r * 128 + ((piece ^ r) << 4), fq);
+            store_row<P>(out + (qo ^ r * 16) + r * 128, fq);
         }
         if (b == 7)
 #pragma unroll
@@ -738,22 +739,24 @@ __global__ void __launch_bounds__(256, 2)
     }
     __syncthreads();
     constexpr int NT = D / 64;  // 8-column tiles of a warp
-    const int ar = lane % 16, ak = lane / 16 * 8;
+    const uint32_t at_b = (uint32_t)(lane % 16 * kRow + b * NT * 8) * 2;
+    const uint32_t at_kg = smem_u32(sm.x.kg.k_hi) + at_b, at_v = smem_u32(sm.l.v) + at_b;
+    const uint32_t at_t = smem_u32(sm.l.t.hi) + (uint32_t)(lane % 16 * 72 + lane / 16 * 8) * 2;
     float acc[4][NT][4] = {}, acu[4][NT][4] = {};
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
         uint32_t bh[NT][2], bl[NT][2], bv[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-            ldsm2t(bh[x], smem_u32(&sm.x.kg.k_hi[ks * 16 + ar][(b * NT + x) * 8]));
-            ldsm2t(bl[x], smem_u32(&sm.x.kg.k_lo[ks * 16 + ar][(b * NT + x) * 8]));
-            ldsm2t(bv[x], smem_u32(&sm.l.v[ks * 16 + ar][(b * NT + x) * 8]));
+            ldsm2t(bh[x], at_kg + (ks * 16 * kRow + x * 8) * 2);
+            ldsm2t(bl[x], at_kg + (64 * kRow + ks * 16 * kRow + x * 8) * 2);
+            ldsm2t(bv[x], at_v + (ks * 16 * kRow + x * 8) * 2);
         }
 #pragma unroll
         for (int m = ks; m < 4; ++m) {
             uint32_t ah[4], al[4];
-            ldsm4(ah, smem_u32(&sm.l.t.hi[m * 16 + ar][ks * 16 + ak]));
-            ldsm4(al, smem_u32(&sm.l.t.lo[m * 16 + ar][ks * 16 + ak]));
+            ldsm4(ah, at_t + (m * 16 * 72 + ks * 16) * 2);
+            ldsm4(al, at_t + (64 * 72 + m * 16 * 72 + ks * 16) * 2);
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
                 mma16(acc[m][x], ah, bh[x]);
@@ -770,13 +773,13 @@ __global__ void __launch_bounds__(256, 2)
         for (int m = 0; m < 4; ++m)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {  // rows g and g + 8 of the tile
-                const float down = sm.down_t[m * 16 + half * 8 + g];
+                const float down = sm.down_t[m * 16 + half * 8 + g], down_w = down * down_k, down_u = down * down_v;
 #pragma unroll
                 for (int x = 0; x < NT; ++x)
 #pragma unroll
                     for (int e = 2 * half; e < 2 * half + 2; ++e) {
-                        acc[m][x][e] = acc[m][x][e] * down * down_k;
-                        acu[m][x][e] = acu[m][x][e] * down * down_v;
+                        acc[m][x][e] *= down_w;
+                        acu[m][x][e] *= down_u;
                         top = fmaxf(top, fabsf(acc[m][x][e]));
                     }
             }
