@@ -197,6 +197,7 @@ struct PrepSmem {
     union {
         struct { __half lk_hi[32][kRow], lk_lo[32][kRow], lq[32][kRow], rk_hi[32][kRow], rk_lo[32][kRow]; } lv;
         struct { __half k_hi[64][kRow], k_lo[64][kRow]; } kg;
+        struct { __half k[64][kRow], q[64][kRow]; } kq;
         char w[2 * Slot<D>::kW];  // W's images: a column block's hi and lo rows, block by block
     } x;
     union {
@@ -352,6 +353,12 @@ __global__ void __launch_bounds__(256, 2)
     float down_k, down_q, down_v;
     {
         // Rows past the end read the last row instead (no branch between the loads) and are masked.
+        // (and the gate's parameters, before anything waits for a load).
+        const float factor = gate_factor(p.a_log, h, p.gate_kind);
+        float bias[C] = {};
+        if (p.dt_bias != nullptr)
+#pragma unroll
+            for (int c = 0; c < C; ++c) bias[c] = p.dt_bias[kChannelGate ? h * D + lane * C + c : h];
         const T *kp = static_cast<const T *>(p.k) + t0 * p.ks[0] + h * p.ks[1] + lane * C;
         const T *qp = static_cast<const T *>(p.q) + t0 * p.qs[0] + h * p.qs[1] + lane * C;
         const T *vp = static_cast<const T *>(p.v) + t0 * p.vs[0] + h * p.vs[1] + lane * C;
@@ -373,16 +380,9 @@ __global__ void __launch_bounds__(256, 2)
             qv[r] = ld_vec<T, C>(qp + row * p.qs[0]);
             vv[r] = ld_vec<T, C>(vp + row * p.vs[0]);
         }
-        if (lane < 8) {
-            const int64_t t = t0 + b * 8 + lane;
-            sm.beta[b * 8 + lane] =
-                b * 8 + lane < n ? beta_of(ld_dyn(p.beta, t * p.bs[0] + h * p.bs[1], p.beta_dtype), p.beta_kind) : 0.0f;
-        }
-        const float factor = gate_factor(p.a_log, h, p.gate_kind);
-        float bias[C] = {};
-        if (p.dt_bias != nullptr)
-#pragma unroll
-            for (int c = 0; c < C; ++c) bias[c] = kChannelGate ? p.dt_bias[h * D + lane * C + c] : p.dt_bias[h];
+        const int64_t tb = t0 + min(b * 8 + lane % 8, n - 1);
+        const float beta = ld_dyn(p.beta, tb * p.bs[0] + h * p.bs[1], p.beta_dtype);
+        if (lane < 8) sm.beta[b * 8 + lane] = b * 8 + lane < n ? beta_of(beta, p.beta_kind) : 0.0f;
         float2 whole[P];
 #pragma unroll
         for (int c = 0; c < P; ++c) whole[c] = make_float2(1.0f, 1.0f);
@@ -452,6 +452,9 @@ __global__ void __launch_bounds__(256, 2)
     constexpr float kDownA = 0x1p-22f;
     const float down_kk = down_k * down_k;
 
+    const int g = lane / 4, cc = lane % 4 * 2;
+    constexpr int kRow = PrepSmem<D>::kRow;
+    if constexpr (kChannelGate) {
     // ---- pairs inside 8 tokens: running products of decays, FP32. For i = 0..7: q_i k_i,
     // then for j < i the pair (k_i k_j, q_i k_j); 64 sums in batches of 16.
     {
@@ -493,8 +496,7 @@ __global__ void __launch_bounds__(256, 2)
 
     // ---- pairs of blocks: per level, the later half's tokens carry the decays
     // from the middle to them, the earlier half's those from them to the middle
-    const int g = lane / 4, cc = lane % 4 * 2;
-    constexpr int kRow = PrepSmem<D>::kRow, kPlane = 32 * kRow * 2;  // bytes from hi to lo
+    constexpr int kPlane = 32 * kRow * 2;  // bytes from hi to lo
     const uint32_t at_lk = smem_u32(sm.x.lv.lk_hi), at_lq = smem_u32(sm.x.lv.lq), at_rk = smem_u32(sm.x.lv.rk_hi);
 #pragma unroll 1
     for (int half = 1; half <= 4; half *= 2) {  // blocks of 8 in half a level: 1, 2, 4
@@ -598,6 +600,59 @@ __global__ void __launch_bounds__(256, 2)
             }
         }
         __syncthreads();
+    }
+    } else {
+    // ---- one decay per token: k_i k_j and q_i k_j need no decayed operands, so k and q as
+    // they are (exact in one half) give both by one product, and the decays between i and
+    // j, products again, multiply the results.
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const int row = b * 8 + r;
+        *reinterpret_cast<Vec<__half2, P> *>(&sm.x.kq.k[row][lane * C]) = *reinterpret_cast<const Vec<__half2, P> *>(&k[r][0]);
+        *reinterpret_cast<Vec<__half2, P> *>(&sm.x.kq.q[row][lane * C]) = *reinterpret_cast<const Vec<__half2, P> *>(&q[r][0]);
+        if (lane == 0) sm.tmp[0][row / 16][row % 16] = a[r][0].x;
+    }
+    __syncthreads();
+    {
+        // sm.T[i][j] = the product of the decays after j up to i, zero above the diagonal:
+        // column j, 16 rows per thread
+        const int j = threadIdx.x % 64, part = threadIdx.x / 64;
+        float run = 1.0f;
+#pragma unroll
+        for (int t = 0; t < 64; ++t) {
+            const float x = sm.tmp[0][t / 16][t % 16];
+            if (t > j) run *= x;
+            if (t / 16 == part) sm.T[t][j] = t >= j ? run : 0.0f;
+        }
+    }
+    __syncthreads();
+    {
+        const uint32_t at_k = smem_u32(sm.x.kq.k), at_q = smem_u32(sm.x.kq.q);
+        for (int tile = b; tile < 20; tile += 8) {  // 16 x 8 tiles on and below the diagonal
+            const int m = (tile >= 2) + (tile >= 6) + (tile >= 12), nt = tile - m * (m + 1);
+            const uint32_t left = (uint32_t)((m * 16 + lane % 16) * kRow + lane / 16 * 8) * 2;
+            const uint32_t right = at_k + (uint32_t)((nt * 8 + lane % 8) * kRow + lane / 8 % 2 * 8) * 2;
+            float ck[4] = {}, cq[4] = {};
+#pragma unroll
+            for (int kk = 0; kk < D; kk += 16) {
+                uint32_t ak[4], aq[4], bk[2];
+                ldsm2(bk, right + kk * 2);
+                ldsm4(ak, at_k + left + kk * 2);
+                ldsm4(aq, at_q + left + kk * 2);
+                mma16(ck, ak, bk);
+                mma16(cq, aq, bk);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = m * 16 + g + e / 2 * 8, j = nt * 8 + cc + e % 2;
+                const float decay = sm.T[i][j];
+                if (i > j) sm.l.L[i][j] = ck[e] * down_kk * decay * sm.beta[i];
+                sm.A[i][j] = __float2half_rn(cq[e] * kDownA * decay);
+            }
+        }
+    }
+    __syncthreads();
+    // T's blocks above the diagonal are zeros again (their decays were), the others are written.
     }
 
     // ---- T = (I + L)^-1, diagonal blocks of 16 by forward substitution, a column per lane
