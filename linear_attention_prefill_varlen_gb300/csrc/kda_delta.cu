@@ -480,14 +480,18 @@ DeltaParams params_of(const kda_delta_t *d) {
     return p;
 }
 
-// Sequences up to this length go token by token, longer ones in chunks.
-#ifndef KDA_SHORT
-#define KDA_SHORT 16
-#endif
-constexpr int kShortLen = KDA_SHORT;
+// Sequences up to this length go four tokens at a time through FP32, longer ones in
+// chunks. Where all (sequence, head) pairs run at once (four blocks of 32 rows each,
+// two per SM) the chunked path's launches cost as much as about 80 tokens; a full
+// GPU does 40 tokens for the price of a chunk (bf16, 12 heads of 128, us: one
+// sequence of 64 tokens 22 against 33, of 128 42 against 36; 256 sequences of 32 362
+// against 494, of 64 682 against 507).
+int short_len(int64_t num_seqs, int64_t heads) {
+    return num_seqs * heads * 4 <= 2 * (int64_t)current_sms() ? 80 : 40;
+}
 
 // Whether a packed call uses the chunked path: 16-bit x and sequences that can be long.
-bool uses_chunks(int64_t tokens, int x_dtype) { return x_dtype != KDA_DTYPE_F32 && tokens > kShortLen; }
+bool uses_chunks(int64_t tokens, int x_dtype, int short_tokens) { return x_dtype != KDA_DTYPE_F32 && tokens > short_tokens; }
 
 // Grids of (sequences x heads) blocks, and token rows, stay below 2^31.
 bool sizes_ok(int64_t tokens, int64_t num_seqs, int64_t heads) {
@@ -511,7 +515,7 @@ kda_status_t kda_packed_delta_rule_workspace(int64_t tokens, int64_t num_seqs, i
         return KDA_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return KDA_ERR_UNSUPPORTED;
     *bytes = 0;
-    if (tokens > 0 && num_seqs > 0 && uses_chunks(tokens, x_dtype))
+    if (tokens > 0 && num_seqs > 0 && uses_chunks(tokens, x_dtype, 40))  // the shorter of the two lengths
         *bytes = chunk_plan(tokens, num_seqs, heads, head_dim, sm_count ? sm_count : current_sms()).bytes;
     return KDA_OK;
 }
@@ -533,14 +537,15 @@ kda_status_t kda_packed_delta_rule(const kda_delta_t *d, int64_t tokens,
     p.null_block_id = null_block_id;
     p.num_seqs = (int)num_seqs;
     p.tokens = tokens;
-    if (!uses_chunks(tokens, d->x_dtype)) return cuda_status(run_op<Recurrent>(p, d, INT32_MAX, nullptr, stream));
+    const int short_tokens = short_len(num_seqs, d->heads);
+    if (!uses_chunks(tokens, d->x_dtype, short_tokens)) return cuda_status(run_op<Recurrent>(p, d, INT32_MAX, nullptr, stream));
     const ChunkPlan plan = chunk_plan(tokens, num_seqs, d->heads, d->head_dim, current_sms());
     if (workspace == nullptr || workspace_bytes < plan.bytes || plan.slots * d->heads > INT32_MAX)
         return KDA_ERR_INVALID_ARG;
     if (!aligned(workspace, 256)) return KDA_ERR_MISALIGNED;
     // The short sequences first: that kernel also zeroes the workspace's head.
-    cudaError_t e = run_op<Recurrent>(p, d, kShortLen, static_cast<int *>(workspace), stream);
-    if (e == cudaSuccess) e = run_chunked(p, d, plan, kShortLen, workspace, stream);
+    cudaError_t e = run_op<Recurrent>(p, d, short_tokens, static_cast<int *>(workspace), stream);
+    if (e == cudaSuccess) e = run_chunked(p, d, plan, short_tokens, workspace, stream);
     return cuda_status(e);
 }
 

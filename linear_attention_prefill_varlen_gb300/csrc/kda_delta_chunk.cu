@@ -618,11 +618,16 @@ __global__ void __launch_bounds__(256, 2)
         // column j, 16 rows per thread
         const int j = threadIdx.x % 64, part = threadIdx.x / 64;
         float run = 1.0f;
+        for (int t = 0; t < part * 16; t += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(&sm.tmp[0][t / 16][t % 16]);
+            run *= (t > j ? x.x : 1.0f) * (t + 1 > j ? x.y : 1.0f);
+            run *= (t + 2 > j ? x.z : 1.0f) * (t + 3 > j ? x.w : 1.0f);
+        }
 #pragma unroll
-        for (int t = 0; t < 64; ++t) {
-            const float x = sm.tmp[0][t / 16][t % 16];
-            if (t > j) run *= x;
-            if (t / 16 == part) sm.T[t][j] = t >= j ? run : 0.0f;
+        for (int i = 0; i < 16; ++i) {
+            const int t = part * 16 + i;
+            run *= t > j ? sm.tmp[0][part][i] : 1.0f;
+            sm.T[t][j] = t >= j ? run : 0.0f;
         }
     }
     __syncthreads();
