@@ -10,6 +10,8 @@
 //
 // Bound: for one token the state, read and written once, in HBM (1024 tokens of
 // 12 heads: 250 us, 6.49 TB/s, 97% of a device copy's rate).
+#include <type_traits>
+
 #include "kda_delta_chunk.cuh"
 
 namespace kda_layer {
@@ -135,243 +137,331 @@ __global__ void __launch_bounds__(kWarps * 32) delta_update_kernel(const __grid_
     }
 }
 
-// ------------------------------------------------------------------ sequences, four tokens at a time
+// ------------------------------------------------------------------ sequences, eight tokens at a time
 
-// With G_j the decays of a block's tokens up to j and H_j those after j,
-//     p_j = S (k_j G_j),  r_j = S (q_j G_j)              all from the block's first S
-//     u_j = beta_j (v_j - p_j - sum_{i<j} u_i M_ji),     M_ji = k_j . (k_i G_j / G_i)
-//     o_j = scale (r_j + sum_{i<=j} u_i N_ji),           N_ji = q_j . (k_i G_j / G_i)
-//     S   = S G_3 + sum_j u_j (k_j H_j)
-// (the quotients are products of the decays between). The state is touched 13
-// times for 4 tokens instead of 16, and one reduction over lanes, not four, stands
-// between a block and the next. The block's threads prepare two such groups at a
-// time in shared memory, a thread per channel. A row belongs to 16 lanes: with 8,
-// shared memory would be read twice as often per product, and it, not the FP32
-// pipe, would bound the loop.
-constexpr int kTokens = 4, kBlocks = 2, kRound = kTokens * kBlocks;
+// With G_j the decays of a group's tokens up to j and H_j those after j, all from
+// the group's first state S (16 rows v per warp):
+//     P = S [k_j G_j],  R = S [q_j G_j]                       16 x 8 each
+//     U = (V - P) T^T,   T = (I + diag(beta) M)^-1 diag(beta), M_ji = k_j . (k_i G_j / G_i), i < j
+//     O = scale (R + U N^T),                                  N_ji = q_j . (k_i G_j / G_i), i <= j
+//     S = S G_7 + U [k_j H_j]
+// (the quotients are products of the decays between). Each product is m16n8k8 in
+// tf32, three times for FP32's accuracy (x = hi + lo with 22 bits; lo lo is left
+// out); R and U N^T, which feed only o, keep 11 bits of the vectors where o has no
+// more than that. The state stays in registers as accumulator fragments: those
+// are operand fragments too when a tile's columns 2 t and 2 t + 1 are taken as the
+// operand's t and t + 4, and the same holds for tokens in P, V - P and U, so
+// nothing moves between lanes.
+//
+// Warps of a block: row warps go through the groups in order; the others prepare
+// groups ahead of them, one warp per group with 8 tokens of every channel in its
+// registers, into slots of shared memory in fragment order (a 16-byte piece per
+// lane and 8-column tile, at piece ^ (tile % 8) against bank conflicts).
+//
+// Bound: the tensor core's tf32 rate (512 multiply-adds per clock and SM): 118
+// products per warp and group are 236 clocks per token and head of 128.
+constexpr int kGroup = 8;
 
-template <int D>
-struct Round {
-    float kd[kRound][D], qd[kRound][D], ku[kRound][D], v[kRound][D], a[kBlocks][D];
-    float part[kBlocks][4][16];  // per warp: M (k) and N (q) sums, pairs in pair_at's order
-    float coef[kBlocks][16];
-    float beta[kRound];
+template <typename T, int D>
+struct GroupSlot {
+    static constexpr int kTiles = D / 8, kQ = sizeof(T) == 4 ? 4 : 2;  // floats of a piece of q: hi (and lo)
+    float kd[kTiles][32][4];   // k_j G_j: hi of two columns, lo of them; lane (token, column pair)
+    float ku[kTiles][32][4];   // k_j H_j: hi of two tokens, lo of them; lane (column, token pair)
+    float qd[kTiles][32][kQ];  // q_j G_j
+    float v[kGroup][D + 4];
+    float a[D];
+    float t[kGroup][kGroup], n[kGroup][kGroup];
 };
 
-// Order of the 16 sums: N_ji for i <= j, then M_ji for i < j.
-__host__ __device__ constexpr int n_at(int j, int i) { return j * (j + 1) / 2 + i; }
-__host__ __device__ constexpr int m_at(int j, int i) { return 10 + j * (j - 1) / 2 + i; }
+template <typename T, int D, int kRowWarps, int kSlots>
+struct RowsSmem {
+    GroupSlot<T, D> slot[kSlots];
+    float m[kSlots][kGroup][kGroup];  // beta_j M_ji, of the warp that prepares the slot
+    uint64_t full[kSlots], empty[kSlots];
+    int abort;
+};
 
-// m tokens of group b of the round.
-template <typename T, int D, int kGroups, int m>
-__device__ __forceinline__ void group(const DeltaParams &p, const Round<D> &sm, int b, float2 (&S)[kGroups][D / 64][2],
-                                      int64_t base, int h, int row0, int lane) {
-    constexpr int NV = D / 64, kDup = 16 / kGroups;
-    const int sub = lane / 16, col = lane % 16;
-    float sums[2][m];
+__device__ __forceinline__ float tf32_hi(float x) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return __uint_as_float(r);
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const float (&a)[4], float b0, float b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
+                   "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+// An accumulator fragment as operand: hi and lo parts, columns 2 t and 2 t + 1 as t and t + 4.
+__device__ __forceinline__ void operand(const float (&c)[4], float (&hi)[4], float (&lo)[4]) {
+    const float x[4] = {c[0], c[2], c[1], c[3]};
 #pragma unroll
-    for (int j = 0; j < m; ++j)
-#pragma unroll
-        for (int what = 0; what < 2; ++what) {
-            const float *x = (what ? sm.qd : sm.kd)[b * kTokens + j];
-            float2 acc[kGroups];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const float4 f = *reinterpret_cast<const float4 *>(x + i * 64 + col * 4);
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    acc[g] = i == 0 ? __fmul2_rn(S[g][i][0], make_float2(f.x, f.y))
-                                    : __ffma2_rn(S[g][i][0], make_float2(f.x, f.y), acc[g]);
-                    acc[g] = __ffma2_rn(S[g][i][1], make_float2(f.z, f.w), acc[g]);
-                }
-            }
-            float v[kGroups];
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) v[g] = acc[g].x + acc[g].y;
-            // Sums over the 16 lanes of a row, group g to lanes kDup g ...
-#pragma unroll
-            for (int w = 8, left = kGroups; w > 0; w /= 2, left = left > 1 ? left / 2 : 1) {
-                if (left > 1) {
-                    const bool up = col & w;
-#pragma unroll
-                    for (int g = 0; g < left / 2; ++g) {
-                        const float send = up ? v[g] : v[g + left / 2], keep = up ? v[g + left / 2] : v[g];
-                        v[g] = keep + __shfl_xor_sync(0xffffffffu, send, w);
-                    }
-                } else {
-                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
-                }
-            }
-            sums[what][j] = v[0];
-        }
-    // The lane's row: its u and o
-    const int row = row0 + col / kDup * 2 + sub;
-    float c[16], u[m];
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(&sm.coef[b][i]);
-        c[i] = f.x, c[i + 1] = f.y, c[i + 2] = f.z, c[i + 3] = f.w;
-    }
-    T *out = static_cast<T *>(p.out) + (base + b * kTokens) * p.os[0] + h * p.os[1] + row;
-#pragma unroll
-    for (int j = 0; j < m; ++j) {
-        float x = sm.v[b * kTokens + j][row] - sums[0][j];
-#pragma unroll
-        for (int i = 0; i < j; ++i) x = fmaf(-u[i], c[m_at(j, i)], x);
-        u[j] = sm.beta[b * kTokens + j] * x;
-        float o = sums[1][j];
-#pragma unroll
-        for (int i = 0; i <= j; ++i) o = fmaf(u[i], c[n_at(j, i)], o);
-        if (col % kDup == j % kDup) out[j * p.os[0]] = from_f<T>(p.scale * o);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const float4 f = *reinterpret_cast<const float4 *>(sm.a[b] + i * 64 + col * 4);
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            S[g][i][0] = __fmul2_rn(S[g][i][0], make_float2(f.x, f.y));
-            S[g][i][1] = __fmul2_rn(S[g][i][1], make_float2(f.z, f.w));
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < m; ++j) {
-        float uj[kGroups];
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) uj[g] = __shfl_sync(0xffffffffu, u[j], sub * 16 + g * kDup);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const float4 f = *reinterpret_cast<const float4 *>(sm.ku[b * kTokens + j] + i * 64 + col * 4);
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                S[g][i][0] = __ffma2_rn(make_float2(uj[g], uj[g]), make_float2(f.x, f.y), S[g][i][0]);
-                S[g][i][1] = __ffma2_rn(make_float2(uj[g], uj[g]), make_float2(f.z, f.w), S[g][i][1]);
-            }
-        }
-    }
+    for (int i = 0; i < 4; ++i) hi[i] = tf32_hi(x[i]), lo[i] = tf32_hi(x[i] - hi[i]);
 }
 
-template <typename T, int D, int kGroups, bool kChannelGate, typename G>
-__global__ void __launch_bounds__(kWarps * 32, 2)
-    delta_recurrent_kernel(const __grid_constant__ DeltaParams p, int max_len, int *head) {
-    constexpr int kRows = kWarps * 2 * kGroups;  // rows of a block
-    constexpr int NV = D / 64;                   // 4-column pieces of a lane's part of a row
-    __shared__ Round<D> sm;
+// Prepares tokens [first, first + 8) of the sequence into a slot: one warp, C channels per lane.
+template <typename T, int D, bool kChannelGate, typename G>
+__device__ __forceinline__ void prepare_group(const DeltaParams &p, const Seq &seq, int64_t first, int h, int lane,
+                                              float factor, const float (&bias)[D / 32], GroupSlot<T, D> &sl,
+                                              float (&bm)[kGroup][kGroup]) {
+    constexpr int C = D / 32, kQ = GroupSlot<T, D>::kQ;
+    const int64_t len = seq.end - seq.start;
+    const int n = (int)min((int64_t)kGroup, len - first);
+    // Rows past the end read the last row instead and are masked.
+    Vec<T, C> kv[8], qv[8], vv[8];
+    Vec<G, C> gv[8];
+    float one[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t t = seq.start + first + min(j, n - 1);
+        if constexpr (kChannelGate)
+            gv[j] = ld_vec<G, C>(static_cast<const G *>(p.gate) + t * p.gs[0] + h * p.gs[1] + lane * C);
+        else
+            one[j] = ld_dyn(p.gate, t * p.gs[0] + h * p.gs[1], p.gate_dtype);
+        kv[j] = ld_vec<T, C>(static_cast<const T *>(p.k) + t * p.ks[0] + h * p.ks[1] + lane * C);
+        qv[j] = ld_vec<T, C>(static_cast<const T *>(p.q) + t * p.qs[0] + h * p.qs[1] + lane * C);
+        vv[j] = ld_vec<T, C>(static_cast<const T *>(p.v) + t * p.vs[0] + h * p.vs[1] + lane * C);
+    }
+    const int64_t tb = seq.start + first + min(lane % 8, n - 1);
+    float beta = beta_of(ld_dyn(p.beta, tb * p.bs[0] + h * p.bs[1], p.beta_dtype), p.beta_kind);
+    if (lane % 8 >= n) beta = 0.0f;
+
+    float a[8][C], k[8][C], q[8][C];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float same = kChannelGate ? 1.0f : decay_of(one[j], p.gate_kind, factor, bias[0]);
+        float v[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            a[j][c] = kChannelGate ? decay_of(to_f<G>(gv[j].v[c]), p.gate_kind, factor, bias[c]) : same;
+            k[j][c] = to_f<T>(kv[j].v[c]), q[j][c] = to_f<T>(qv[j].v[c]), v[c] = to_f<T>(vv[j].v[c]);
+            if (j >= n) a[j][c] = 1.0f, k[j][c] = q[j][c] = v[c] = 0.0f;
+        }
+        if constexpr (C == 4) *reinterpret_cast<float4 *>(&sl.v[j][lane * C]) = make_float4(v[0], v[1], v[2], v[3]);
+        else *reinterpret_cast<float2 *>(&sl.v[j][lane * C]) = make_float2(v[0], v[1]);
+    }
+    // M and N: 64 sums over the channels, in batches of 16. For i = 0..7: q_i k_i, then for
+    // j < i k_i k_j and q_i k_j, with k_j decayed to token i.
+    {
+        float f[16], w[8][C];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) w[i][c] = k[i][c];
+#pragma unroll
+            for (int e = 0; e <= 2 * i; ++e) {
+                const int j = e == 0 ? i : (e - 1) / 2;
+                float sum = 0.0f;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    if (e % 2 == 1) w[j][c] *= a[i][c];
+                    sum = fmaf(e % 2 == 1 ? k[i][c] : q[i][c], w[j][c], sum);
+                }
+                const int at = i * i + e;
+                f[at % 16] = sum;
+                if (at % 16 == 15) {
+                    const float got = scatter_sum(f, lane);
+                    const int mine = at - 15 + lane / 2;
+                    const int row = (mine >= 1) + (mine >= 4) + (mine >= 9) + (mine >= 16) + (mine >= 25) +
+                                    (mine >= 36) + (mine >= 49);
+                    const int own = mine - row * row, col = own == 0 ? row : (own - 1) / 2;
+                    const float b = __shfl_sync(0xffffffffu, beta, row);
+                    if (own % 2 == 1) {
+                        bm[row][col] = got * b;
+                    } else {
+                        sl.n[row][col] = got;
+                        if (col < row) sl.n[col][row] = 0.0f;
+                    }
+                }
+            }
+        }
+    }
+    // The vectors, decayed from the group's start and to its end, as fragments
+    float run[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) run[c] = 1.0f;
+    const int tile = lane * C / 8, sw = tile % 8, in_tile = lane * C % 8;  // first column in its tile
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int c = 0; c < C; c += 2) {
+            float kd[2], qd[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                run[c + x] *= a[j][c + x];
+                kd[x] = k[j][c + x] * run[c + x], qd[x] = q[j][c + x] * run[c + x];
+            }
+            const int piece = (j * 4 + (in_tile + c) / 2) ^ sw;
+            const float h0 = tf32_hi(kd[0]), h1 = tf32_hi(kd[1]);
+            *reinterpret_cast<float4 *>(sl.kd[tile][piece]) = make_float4(h0, h1, tf32_hi(kd[0] - h0), tf32_hi(kd[1] - h1));
+            const float g0 = tf32_hi(qd[0]), g1 = tf32_hi(qd[1]);
+            if constexpr (kQ == 4)
+                *reinterpret_cast<float4 *>(sl.qd[tile][piece]) = make_float4(g0, g1, tf32_hi(qd[0] - g0), tf32_hi(qd[1] - g1));
+            else
+                *reinterpret_cast<float2 *>(sl.qd[tile][piece]) = make_float2(g0, g1);
+        }
+    if constexpr (C == 4) *reinterpret_cast<float4 *>(&sl.a[lane * C]) = make_float4(run[0], run[1], run[2], run[3]);
+    else *reinterpret_cast<float2 *>(&sl.a[lane * C]) = make_float2(run[0], run[1]);
+#pragma unroll
+    for (int c = 0; c < C; ++c) run[c] = 1.0f;
+#pragma unroll
+    for (int j = 6; j >= 0; j -= 2)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float later = k[j + 1][c] * run[c];
+            run[c] *= a[j + 1][c];
+            const float sooner = k[j][c] * run[c];
+            run[c] *= a[j][c];
+            const float h0 = tf32_hi(sooner), h1 = tf32_hi(later);
+            const int piece = ((in_tile + c) * 4 + j / 2) ^ sw;
+            *reinterpret_cast<float4 *>(sl.ku[tile][piece]) = make_float4(h0, h1, tf32_hi(sooner - h0), tf32_hi(later - h1));
+        }
+    // T, a column per lane, by forward substitution
+    __syncwarp();
+    if (lane < 8) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float sum = i == lane ? beta : 0.0f;
+#pragma unroll
+            for (int m = 0; m < i; ++m) sum = fmaf(-bm[i][m], x[m], sum);
+            x[i] = i < lane ? 0.0f : sum;
+            sl.t[i][lane] = x[i];
+        }
+    }
+    __syncwarp();
+}
+
+template <typename T, int D, int kRowWarps, int kSlots, bool kChannelGate, typename G>
+__global__ void __launch_bounds__((kRowWarps + kSlots) * 32, 1)
+    delta_rows_kernel(const __grid_constant__ DeltaParams p, int min_len, int max_len, int *head) {
+    using Sm = RowsSmem<T, D, kRowWarps, kSlots>;
+    using Slot = GroupSlot<T, D>;
+    constexpr int kTiles = D / 8;
+    // Terms of a product that feeds only o: all of FP32's for FP32, the state's lo for fp16.
+    constexpr int kWide = sizeof(T) == 4 ? 3 : std::is_same<T, __half>::value ? 2 : 1;
+    extern __shared__ __align__(16) char raw_smem[];
+    Sm &sm = *reinterpret_cast<Sm *>(raw_smem);
     dependency_wait();
     // The head of the chunked path's workspace, before its kernels use it.
     if (head != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 64) head[threadIdx.x] = 0;
     const int s = blockIdx.x / p.heads, h = blockIdx.x % p.heads;
     const Seq seq = load_seq(p, s);
     const int64_t len = seq.end - seq.start;
-    if (len <= 0 || len > max_len) return;
+    if (len < min_len || len > max_len) return;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int sub = lane / 16, col = lane % 16;
-    const int row0 = blockIdx.y * kRows + warp * 2 * kGroups;
-    float *state = p.states + (seq.line < 0 ? 0 : seq.line) * p.ss[0] + h * p.ss[1];
-
-    // Preparation: channel d of group blk of the round. Rows past the end read the
-    // last row instead and are masked.
-    const int d = threadIdx.x % D, blk = threadIdx.x / D;
-    const bool prepares = D * kBlocks == kWarps * 32 || blk < kBlocks;
-    T qr[kTokens], kr[kTokens], vr[kTokens];
-    G gr[kTokens];
-    float one[kTokens], br = 0.0f;
-    auto load = [&](int64_t first) {
-#pragma unroll
-        for (int j = 0; j < kTokens; ++j) {
-            const int64_t t = seq.start + min(first + blk * kTokens + j, len - 1);
-            qr[j] = static_cast<const T *>(p.q)[t * p.qs[0] + h * p.qs[1] + d];
-            kr[j] = static_cast<const T *>(p.k)[t * p.ks[0] + h * p.ks[1] + d];
-            vr[j] = static_cast<const T *>(p.v)[t * p.vs[0] + h * p.vs[1] + d];
-            if constexpr (kChannelGate) gr[j] = static_cast<const G *>(p.gate)[t * p.gs[0] + h * p.gs[1] + d];
-            else one[j] = ld_dyn(p.gate, t * p.gs[0] + h * p.gs[1], p.gate_dtype);
+    const int64_t groups = (len + kGroup - 1) / kGroup;
+    volatile int *abort = &sm.abort;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            bar_init(smem_u32(&sm.full[i]), 1);
+            bar_init(smem_u32(&sm.empty[i]), kRowWarps);
         }
-        const int64_t t = seq.start + min(first + (int)(threadIdx.x % kRound), len - 1);
-        br = ld_dyn(p.beta, t * p.bs[0] + h * p.bs[1], p.beta_dtype);
-    };
-    load(0);
-    float2 S[kGroups][NV][2];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-        const float *row = state + (row0 + g * 2 + sub) * D;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (seq.reads) f = *reinterpret_cast<const float4 *>(row + i * 64 + col * 4);
-            S[g][i][0] = make_float2(f.x, f.y), S[g][i][1] = make_float2(f.z, f.w);
-        }
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const float factor = gate_factor(p.a_log, h, p.gate_kind);
-    const float bias = p.dt_bias == nullptr ? 0.0f : kChannelGate ? p.dt_bias[h * D + d] : p.dt_bias[h];
-
-    for (int64_t base = 0; base < len; base += kRound) {
-        const int n = (int)min((int64_t)kRound, len - base);
-        if (base != 0) __syncthreads();
-        if (prepares) {
-            float a[kTokens], k[kTokens], q[kTokens];
-            float run = 1.0f, f[16];
+    __syncthreads();
+    if (warp >= kRowWarps) {
+        const int slot = warp - kRowWarps;
+        const float factor = gate_factor(p.a_log, h, p.gate_kind);
+        float bias[D / 32] = {};
+        if (p.dt_bias != nullptr)
 #pragma unroll
-            for (int j = 0; j < kTokens; ++j) {
-                const int at = blk * kTokens + j;
-                const bool in = at < n;
-                const float decay = decay_of(kChannelGate ? to_f<G>(gr[j]) : one[j], p.gate_kind, factor, bias);
-                a[j] = in ? decay : 1.0f;
-                k[j] = in ? to_f<T>(kr[j]) : 0.0f;
-                q[j] = in ? to_f<T>(qr[j]) : 0.0f;
-                run *= a[j];
-                sm.kd[at][d] = k[j] * run;
-                sm.qd[at][d] = q[j] * run;
-                sm.v[at][d] = in ? to_f<T>(vr[j]) : 0.0f;
-            }
-            sm.a[blk][d] = run;
-            run = 1.0f;
-#pragma unroll
-            for (int j = kTokens - 1; j >= 0; --j) {
-                sm.ku[blk * kTokens + j][d] = k[j] * run;
-                run *= a[j];
-            }
-#pragma unroll
-            for (int i = 0; i < kTokens; ++i) {
-                float w = k[i];
-                f[n_at(i, i)] = q[i] * w;
-#pragma unroll
-                for (int j = i + 1; j < kTokens; ++j) {
-                    w *= a[j];
-                    f[n_at(j, i)] = q[j] * w;
-                    f[m_at(j, i)] = k[j] * w;
-                }
-            }
-            const float sum = scatter_sum(f, lane);
-            if (lane % 2 == 0) sm.part[blk][warp % (D / 32)][lane / 2] = sum;
-            if (threadIdx.x < kRound) sm.beta[threadIdx.x] = (int)threadIdx.x < n ? beta_of(br, p.beta_kind) : 0.0f;
+            for (int c = 0; c < D / 32; ++c) bias[c] = p.dt_bias[kChannelGate ? h * D + lane * (D / 32) + c : h];
+        uint32_t use = 0;
+        for (int64_t g = slot; g < groups; g += kSlots, ++use) {
+            // (A wait that runs out, never in a correct run, ends the block: its rows stay unwritten.)
+            if (use > 0 && !bar_wait(smem_u32(&sm.empty[slot]), (use - 1) & 1, abort)) return;
+            prepare_group<T, D, kChannelGate, G>(p, seq, g * kGroup, h, lane, factor, bias, sm.slot[slot], sm.m[slot]);
+            if (lane == 0) bar_arrive(smem_u32(&sm.full[slot]));
         }
-        // The next round's tokens, while these are worked on (without a branch, at whose
-        // end the loaded registers would be waited for; past the end, the last row again).
-        load(base + kRound);
-        __syncthreads();
-        if (threadIdx.x < kBlocks * 16) {
-            float sum = 0.0f;
+        return;
+    }
+    // ---- row warps
+    const int g = lane / 4, t = lane % 4;
+    const int row = (blockIdx.y * kRowWarps + warp) * 16 + g;  // and row + 8
+    float *state = p.states + (seq.line < 0 ? 0 : seq.line) * p.ss[0] + h * p.ss[1] + row * D + 2 * t;
+    float S[kTiles][4];
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) sum += sm.part[threadIdx.x / 16][x][threadIdx.x % 16];
-            sm.coef[threadIdx.x / 16][threadIdx.x % 16] = sum;
+    for (int n = 0; n < kTiles; ++n) {
+        float2 x = make_float2(0.0f, 0.0f), y = x;
+        if (seq.reads) {
+            x = *reinterpret_cast<const float2 *>(state + n * 8);
+            y = *reinterpret_cast<const float2 *>(state + 8 * D + n * 8);
         }
-        __syncthreads();
-        for (int b = 0; b * kTokens < n; ++b) {
-            const int m = min(kTokens, n - b * kTokens);
-            // Whole groups in straight line, so that the sums of all tokens overlap.
-            if (m == kTokens) group<T, D, kGroups, kTokens>(p, sm, b, S, seq.start + base, h, row0, lane);
-            else if (m == 1) group<T, D, kGroups, 1>(p, sm, b, S, seq.start + base, h, row0, lane);
-            else if (m == 2) group<T, D, kGroups, 2>(p, sm, b, S, seq.start + base, h, row0, lane);
-            else group<T, D, kGroups, 3>(p, sm, b, S, seq.start + base, h, row0, lane);
+        S[n][0] = x.x, S[n][1] = x.y, S[n][2] = y.x, S[n][3] = y.y;
+    }
+    int slot = 0;
+    uint32_t use = 0;
+    for (int64_t grp = 0; grp < groups; ++grp) {
+        if (!bar_wait(smem_u32(&sm.full[slot]), use & 1, abort)) return;
+        const Slot &sl = sm.slot[slot];
+        float P0[2][4] = {}, P1[4] = {}, P2[4] = {}, R0[4] = {}, R1[4] = {}, R2[4] = {};
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+            float hi[4], lo[4];
+            operand(S[n], hi, lo);
+            const float4 b = *reinterpret_cast<const float4 *>(sl.kd[n][lane ^ (n % 8)]);
+            mma_tf32(P0[n % 2], hi, b.x, b.y);
+            mma_tf32(P1, lo, b.x, b.y);
+            mma_tf32(P2, hi, b.z, b.w);
+            if constexpr (Slot::kQ == 4) {
+                const float4 c = *reinterpret_cast<const float4 *>(sl.qd[n][lane ^ (n % 8)]);
+                mma_tf32(R0, hi, c.x, c.y);
+                mma_tf32(R1, lo, c.x, c.y);
+                mma_tf32(R2, hi, c.z, c.w);
+            } else {
+                const float2 c = *reinterpret_cast<const float2 *>(sl.qd[n][lane ^ (n % 8)]);
+                mma_tf32(R0, hi, c.x, c.y);
+                if constexpr (kWide == 2) mma_tf32(R1, lo, c.x, c.y);
+            }
         }
+        float x[4], U[4] = {}, U1[4] = {}, U2[4] = {}, hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = sl.v[2 * t + e % 2][row + e / 2 * 8] - (P0[0][e] + P0[1][e] + (P1[e] + P2[e]));
+        operand(x, hi, lo);
+        {
+            const float2 b = *reinterpret_cast<const float2 *>(&sl.t[g][2 * t]);
+            const float h0 = tf32_hi(b.x), h1 = tf32_hi(b.y);
+            mma_tf32(U, hi, h0, h1);
+            mma_tf32(U1, lo, h0, h1);
+            mma_tf32(U2, hi, tf32_hi(b.x - h0), tf32_hi(b.y - h1));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) U[e] += U1[e] + U2[e], R0[e] += R1[e] + R2[e];
+        operand(U, hi, lo);
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+            const float2 a = *reinterpret_cast<const float2 *>(&sl.a[n * 8 + 2 * t]);
+            const float4 b = *reinterpret_cast<const float4 *>(sl.ku[n][lane ^ (n % 8)]);
+            float add[4] = {};  // apart from S: the tensor core cuts off its sums, FMA rounds them
+            mma_tf32(add, lo, b.x, b.y);
+            mma_tf32(add, hi, b.z, b.w);
+            mma_tf32(add, hi, b.x, b.y);
+            S[n][0] = fmaf(S[n][0], a.x, add[0]), S[n][1] = fmaf(S[n][1], a.y, add[1]);
+            S[n][2] = fmaf(S[n][2], a.x, add[2]), S[n][3] = fmaf(S[n][3], a.y, add[3]);
+        }
+        {
+            const float2 b = *reinterpret_cast<const float2 *>(&sl.n[g][2 * t]);
+            const float h0 = tf32_hi(b.x), h1 = tf32_hi(b.y);
+            mma_tf32(R0, hi, h0, h1);
+            if constexpr (kWide >= 2) mma_tf32(R0, lo, h0, h1);
+            if constexpr (kWide == 3) mma_tf32(R0, hi, tf32_hi(b.x - h0), tf32_hi(b.y - h1));
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_u32(&sm.empty[slot]));
+        const int64_t first = grp * kGroup;
+        T *out = static_cast<T *>(p.out) + (seq.start + first) * p.os[0] + h * p.os[1] + row;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (first + 2 * t + e % 2 < len) out[(2 * t + e % 2) * p.os[0] + e / 2 * 8] = from_f<T>(p.scale * R0[e]);
+        if (++slot == kSlots) slot = 0, ++use;
     }
     if (seq.line < 0) return;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-        float *row = state + (row0 + g * 2 + sub) * D;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            *reinterpret_cast<float4 *>(row + i * 64 + col * 4) =
-                make_float4(S[g][i][0].x, S[g][i][0].y, S[g][i][1].x, S[g][i][1].y);
+    for (int n = 0; n < kTiles; ++n) {
+        *reinterpret_cast<float2 *>(state + n * 8) = make_float2(S[n][0], S[n][1]);
+        *reinterpret_cast<float2 *>(state + 8 * D + n * 8) = make_float2(S[n][2], S[n][3]);
     }
 }
 
@@ -393,13 +483,21 @@ struct Update {
 
 template <typename T, int D, bool kChannelGate, typename G>
 struct Recurrent {
-    static cudaError_t run(const DeltaParams &p, int max_len, int *head, kda_stream_t stream) {
+    template <int kRowWarps, int kSlots>
+    static cudaError_t rows(const DeltaParams &p, int min_len, int max_len, int *head, kda_stream_t stream) {
+        auto *kernel = delta_rows_kernel<T, D, kRowWarps, kSlots, kChannelGate, G>;
+        constexpr size_t smem = sizeof(RowsSmem<T, D, kRowWarps, kSlots>);
+        static_assert(smem <= 232448, "227 KB per block");
+        static std::atomic<uint64_t> done;
+        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), (int)smem, done);
+        if (e != cudaSuccess) return e;
         const unsigned pairs = (unsigned)((int64_t)p.num_seqs * p.heads);
-        if (few_pairs(p))
-            return launch(delta_recurrent_kernel<T, D, 2, kChannelGate, G>, dim3(pairs, D / 32), kWarps * 32, 0, stream,
-                          p, max_len, head);
-        return launch(delta_recurrent_kernel<T, D, D / 16, kChannelGate, G>, dim3(pairs), kWarps * 32, 0, stream, p,
+        return launch(kernel, dim3(pairs, D / (kRowWarps * 16)), (kRowWarps + kSlots) * 32, smem, stream, p, min_len,
                       max_len, head);
+    }
+    static cudaError_t run(const DeltaParams &p, int max_len, int *head, kda_stream_t stream) {
+        if (few_pairs(p)) return rows<D / 32, 6>(p, 1, max_len, head, stream);
+        return rows<D / 16, 4>(p, 1, max_len, head, stream);
     }
 };
 

@@ -107,9 +107,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 // ------------------------------------------------------------------ mma.sync
 
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
@@ -888,33 +885,6 @@ __global__ void __launch_bounds__(256, 2)
 
 // ------------------------------------------------------------------ barriers
 
-// Every wait ends: after kWaitTries polls it gives up and sets `abort`, which
-// ends the other waits of the block too.
-constexpr int kWaitTries = 1 << 20;
-
-__device__ __forceinline__ void bar_init(uint32_t bar, int count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-                 "selp.u32 %0, 1, 0, p;\n}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    for (int i = 0; i < kWaitTries; ++i) {
-        if (bar_test(bar, parity)) return true;
-        if ((i & 63) == 63 && *abort != 0) return false;
-    }
-    *abort = 1;
-    return false;
-}
 // kCount threads meet at barrier kId; true if any of them brings true.
 template <int kId, int kCount>
 __device__ __forceinline__ bool meet_any(bool bad) {
