@@ -327,52 +327,38 @@ __device__ __forceinline__ void prepare_group(const DeltaParams &p, const Seq &s
     __syncwarp();
 }
 
+// The groups of one pair that fall to slot `slot`: turn, turn + 1, ... of the block's groups.
 template <typename T, int D, int kRowWarps, int kSlots, bool kChannelGate, typename G>
-__global__ void __launch_bounds__((kRowWarps + kSlots) * 32, 1)
-    delta_rows_kernel(const __grid_constant__ DeltaParams p, int min_len, int max_len, int *head) {
-    using Sm = RowsSmem<T, D, kRowWarps, kSlots>;
+__device__ __forceinline__ bool prepare_pair(const DeltaParams &p, RowsSmem<T, D, kRowWarps, kSlots> &sm, const Seq &seq,
+                                             int h, int slot, int lane, uint32_t turn, uint32_t groups) {
+    const uint32_t first = (slot + kSlots - turn % kSlots) % kSlots;
+    if (first >= groups) return true;
+    const float factor = gate_factor(p.a_log, h, p.gate_kind);
+    float bias[D / 32] = {};
+    if (p.dt_bias != nullptr)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) bias[c] = p.dt_bias[kChannelGate ? h * D + lane * (D / 32) + c : h];
+    if (first == 0 && lane == 0 && seq.reads)  // the pair's state, on its way to the row warps
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.states + seq.line * p.ss[0] + h * p.ss[1]),
+                     "r"(D * D * 4) : "memory");
+    for (uint32_t g = first; g < groups; g += kSlots) {
+        const uint32_t use = (turn + g) / kSlots;  // of the slot
+        if (use > 0 && !bar_wait(smem_u32(&sm.empty[slot]), (use - 1) & 1, &sm.abort)) return false;
+        prepare_group<T, D, kChannelGate, G>(p, seq, (int64_t)g * kGroup, h, lane, factor, bias, sm.slot[slot], sm.m[slot]);
+        if (lane == 0) bar_arrive(smem_u32(&sm.full[slot]));
+    }
+    return true;
+}
+
+// One pair's groups on this warp's 16 rows.
+template <typename T, int D, int kRowWarps, int kSlots>
+__device__ __forceinline__ bool walk_pair(const DeltaParams &p, RowsSmem<T, D, kRowWarps, kSlots> &sm, const Seq &seq,
+                                          int h, int warp, int lane, uint32_t turn, uint32_t groups) {
     using Slot = GroupSlot<T, D>;
     constexpr int kTiles = D / 8;
     // Terms of a product that feeds only o: all of FP32's for FP32, the state's lo for fp16.
     constexpr int kWide = sizeof(T) == 4 ? 3 : std::is_same<T, __half>::value ? 2 : 1;
-    extern __shared__ __align__(16) char raw_smem[];
-    Sm &sm = *reinterpret_cast<Sm *>(raw_smem);
-    dependency_wait();
-    // The head of the chunked path's workspace, before its kernels use it.
-    if (head != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 64) head[threadIdx.x] = 0;
-    const int s = blockIdx.x / p.heads, h = blockIdx.x % p.heads;
-    const Seq seq = load_seq(p, s);
     const int64_t len = seq.end - seq.start;
-    if (len < min_len || len > max_len) return;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t groups = (len + kGroup - 1) / kGroup;
-    volatile int *abort = &sm.abort;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            bar_init(smem_u32(&sm.full[i]), 1);
-            bar_init(smem_u32(&sm.empty[i]), kRowWarps);
-        }
-        sm.abort = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncthreads();
-    if (warp >= kRowWarps) {
-        const int slot = warp - kRowWarps;
-        const float factor = gate_factor(p.a_log, h, p.gate_kind);
-        float bias[D / 32] = {};
-        if (p.dt_bias != nullptr)
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) bias[c] = p.dt_bias[kChannelGate ? h * D + lane * (D / 32) + c : h];
-        uint32_t use = 0;
-        for (int64_t g = slot; g < groups; g += kSlots, ++use) {
-            // (A wait that runs out, never in a correct run, ends the block: its rows stay unwritten.)
-            if (use > 0 && !bar_wait(smem_u32(&sm.empty[slot]), (use - 1) & 1, abort)) return;
-            prepare_group<T, D, kChannelGate, G>(p, seq, g * kGroup, h, lane, factor, bias, sm.slot[slot], sm.m[slot]);
-            if (lane == 0) bar_arrive(smem_u32(&sm.full[slot]));
-        }
-        return;
-    }
-    // ---- row warps
     const int g = lane / 4, t = lane % 4;
     const int row = (blockIdx.y * kRowWarps + warp) * 16 + g;  // and row + 8
     float *state = p.states + (seq.line < 0 ? 0 : seq.line) * p.ss[0] + h * p.ss[1] + row * D + 2 * t;
@@ -386,10 +372,9 @@ __global__ void __launch_bounds__((kRowWarps + kSlots) * 32, 1)
         }
         S[n][0] = x.x, S[n][1] = x.y, S[n][2] = y.x, S[n][3] = y.y;
     }
-    int slot = 0;
-    uint32_t use = 0;
-    for (int64_t grp = 0; grp < groups; ++grp) {
-        if (!bar_wait(smem_u32(&sm.full[slot]), use & 1, abort)) return;
+    for (uint32_t grp = 0; grp < groups; ++grp) {
+        const uint32_t slot = (turn + grp) % kSlots, use = (turn + grp) / kSlots;
+        if (!bar_wait(smem_u32(&sm.full[slot]), use & 1, &sm.abort)) return false;
         const Slot &sl = sm.slot[slot];
         float P0[2][4] = {}, P1[4] = {}, P2[4] = {}, R0[4] = {}, R1[4] = {}, R2[4] = {};
 #pragma unroll
@@ -445,18 +430,67 @@ __global__ void __launch_bounds__((kRowWarps + kSlots) * 32, 1)
         }
         __syncwarp();
         if (lane == 0) bar_arrive(smem_u32(&sm.empty[slot]));
-        const int64_t first = grp * kGroup;
+        const int64_t first = (int64_t)grp * kGroup;
         T *out = static_cast<T *>(p.out) + (seq.start + first) * p.os[0] + h * p.os[1] + row;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (first + 2 * t + e % 2 < len) out[(2 * t + e % 2) * p.os[0] + e / 2 * 8] = from_f<T>(p.scale * R0[e]);
-        if (++slot == kSlots) slot = 0, ++use;
     }
-    if (seq.line < 0) return;
+    if (seq.line < 0) return true;
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
         *reinterpret_cast<float2 *>(state + n * 8) = make_float2(S[n][0], S[n][1]);
         *reinterpret_cast<float2 *>(state + 8 * D + n * 8) = make_float2(S[n][2], S[n][3]);
+    }
+    return true;
+}
+
+template <typename T, int D, int kRowWarps, int kSlots, bool kChannelGate, typename G>
+__global__ void __launch_bounds__((kRowWarps + kSlots) * 32, 1)
+    delta_rows_kernel(const __grid_constant__ DeltaParams p, int min_len, int max_len, int *head) {
+    using Sm = RowsSmem<T, D, kRowWarps, kSlots>;
+    extern __shared__ __align__(16) char raw_smem[];
+    Sm &sm = *reinterpret_cast<Sm *>(raw_smem);
+    dependency_wait();
+    // The head of the chunked path's workspace, before its kernels use it.
+    if (head != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 64) head[threadIdx.x] = 0;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    volatile int *abort = &sm.abort;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            bar_init(smem_u32(&sm.full[i]), 1);
+            bar_init(smem_u32(&sm.empty[i]), kRowWarps);
+        }
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    // The block's (sequence, head) pairs, one of each gridDim.x, 32 looked at a time. Every
+    // warp goes through the same ones; the slots' turns run on from pair to pair.
+    const int64_t pairs = (int64_t)p.num_seqs * p.heads;
+    const bool prepares = warp >= kRowWarps;
+    uint32_t turn = 0;  // groups of the pairs before
+    for (int64_t base = blockIdx.x; base < pairs; base += 32 * (int64_t)gridDim.x) {
+        const int64_t mine = base + lane * (int64_t)gridDim.x;
+        Seq own = {};
+        if (mine < pairs) own = load_seq(p, (int)(mine / p.heads));
+        uint32_t todo = __ballot_sync(0xffffffffu, own.end - own.start >= min_len && own.end - own.start <= max_len);
+        for (; todo != 0; todo &= todo - 1) {
+            const int from = __ffs(todo) - 1;
+            Seq seq;
+            seq.start = __shfl_sync(0xffffffffu, (int)own.start, from);
+            seq.end = __shfl_sync(0xffffffffu, (int)own.end, from);
+            seq.line = __shfl_sync(0xffffffffu, (int)own.line, from);
+            seq.reads = __shfl_sync(0xffffffffu, (int)own.reads, from) != 0;
+            const int h = (int)((base + from * (int64_t)gridDim.x) % p.heads);
+            const uint32_t groups = (uint32_t)((seq.end - seq.start + kGroup - 1) / kGroup);
+            bool ok;
+            // (A wait that runs out, never in a correct run, ends the block: its rows stay unwritten.)
+            if (prepares) ok = prepare_pair<T, D, kRowWarps, kSlots, kChannelGate, G>(p, sm, seq, h, warp - kRowWarps, lane, turn, groups);
+            else ok = walk_pair<T, D, kRowWarps, kSlots>(p, sm, seq, h, warp, lane, turn, groups);
+            if (!ok) return;
+            turn += groups;
+        }
     }
 }
 
@@ -486,12 +520,14 @@ struct Recurrent {
         static std::atomic<uint64_t> done;
         const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), (int)smem, done);
         if (e != cudaSuccess) return e;
-        const unsigned pairs = (unsigned)((int64_t)p.num_seqs * p.heads);
-        return launch(kernel, dim3(pairs, D / (kRowWarps * 16)), (kRowWarps + kSlots) * 32, smem, stream, p, min_len,
-                      max_len, head);
+        constexpr int kParts = D / (kRowWarps * 16);
+        const int64_t pairs = (int64_t)p.num_seqs * p.heads, room = current_sms() / kParts;
+        return launch(kernel, dim3((unsigned)(pairs < room ? pairs : room), kParts), (kRowWarps + kSlots) * 32, smem,
+                      stream, p, min_len, max_len, head);
     }
     static cudaError_t run(const DeltaParams &p, int max_len, int *head, kda_stream_t stream) {
-        if (few_pairs(p)) return rows<D / 32, 6>(p, 1, max_len, head, stream);
+        // Two blocks of half the rows per pair while all pairs run at once.
+        if ((int64_t)p.num_seqs * p.heads * 2 <= current_sms()) return rows<D / 32, 6>(p, 1, max_len, head, stream);
         return rows<D / 16, 4>(p, 1, max_len, head, stream);
     }
 };
