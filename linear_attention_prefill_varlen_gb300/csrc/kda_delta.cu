@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_update_kernel(const __grid_
     dependency_wait();
     const int s = blockIdx.x / p.heads, h = blockIdx.x % p.heads;
     const Seq seq = load_seq(p, s);
+    if (seq.end - seq.start != 1) return;  // of a packed batch: its one-token sequences
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int sub = lane / 8, col = lane % 8;
     const int row0 = blockIdx.y * kRows + warp * 4 * kGroups;
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_update_kernel(const __grid_
         }
     }
     if (warp == 0) {
-        const int64_t t = s;
+        const int64_t t = seq.start;
         const float factor = gate_factor(p.a_log, h, p.gate_kind);
         float bias[C] = {};
         if (p.dt_bias != nullptr)
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_update_kernel(const __grid_
         pk[g] = u;
     }
     if (col < kGroups)
-        static_cast<T *>(p.out)[(int64_t)s * p.os[0] + h * p.os[1] + row0 + col * 4 + sub] = from_f<T>(o);
+        static_cast<T *>(p.out)[seq.start * p.os[0] + h * p.os[1] + row0 + col * 4 + sub] = from_f<T>(o);
     if (seq.line < 0) return;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
@@ -194,21 +195,19 @@ __device__ __forceinline__ void operand(const float (&c)[4], float (&hi)[4], flo
     for (int i = 0; i < 4; ++i) hi[i] = tf32_hi(x[i]), lo[i] = tf32_hi(x[i] - hi[i]);
 }
 
-// Prepares tokens [first, first + 8) of the sequence into a slot: one warp, C channels per lane.
+// Prepares the group of n tokens at first_row into a slot: one warp, C channels per lane.
 template <typename T, int D, bool kChannelGate, typename G>
-__device__ __forceinline__ void prepare_group(const DeltaParams &p, const Seq &seq, int64_t first, int h, int lane,
+__device__ __forceinline__ void prepare_group(const DeltaParams &p, int first_row, int n, int h, int lane,
                                               float factor, const float (&bias)[D / 32], GroupSlot<T, D> &sl,
                                               float (&bm)[kGroup][kGroup]) {
     constexpr int C = D / 32, kQ = GroupSlot<T, D>::kQ;
-    const int64_t len = seq.end - seq.start;
-    const int n = (int)min((int64_t)kGroup, len - first);
     // Rows past the end read the last row instead and are masked.
     Vec<T, C> kv[8], qv[8], vv[8];
     Vec<G, C> gv[8];
     float one[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int64_t t = seq.start + first + min(j, n - 1);
+        const int64_t t = first_row + min(j, n - 1);
         if constexpr (kChannelGate)
             gv[j] = ld_vec<G, C>(static_cast<const G *>(p.gate) + t * p.gs[0] + h * p.gs[1] + lane * C);
         else
@@ -217,7 +216,7 @@ __device__ __forceinline__ void prepare_group(const DeltaParams &p, const Seq &s
         qv[j] = ld_vec<T, C>(static_cast<const T *>(p.q) + t * p.qs[0] + h * p.qs[1] + lane * C);
         vv[j] = ld_vec<T, C>(static_cast<const T *>(p.v) + t * p.vs[0] + h * p.vs[1] + lane * C);
     }
-    const int64_t tb = seq.start + first + min(lane % 8, n - 1);
+    const int64_t tb = first_row + min(lane % 8, n - 1);
     float beta = beta_of(ld_dyn(p.beta, tb * p.bs[0] + h * p.bs[1], p.beta_dtype), p.beta_kind);
     if (lane % 8 >= n) beta = 0.0f;
 
@@ -341,10 +340,12 @@ __device__ __forceinline__ bool prepare_pair(const DeltaParams &p, RowsSmem<T, D
     if (first == 0 && lane == 0 && seq.reads)  // the pair's state, on its way to the row warps
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.states + seq.line * p.ss[0] + h * p.ss[1]),
                      "r"(D * D * 4) : "memory");
+    const int start = (int)seq.start, end = (int)seq.end;
     for (uint32_t g = first; g < groups; g += kSlots) {
         const uint32_t use = (turn + g) / kSlots;  // of the slot
         if (use > 0 && !bar_wait(smem_u32(&sm.empty[slot]), (use - 1) & 1, &sm.abort)) return false;
-        prepare_group<T, D, kChannelGate, G>(p, seq, (int64_t)g * kGroup, h, lane, factor, bias, sm.slot[slot], sm.m[slot]);
+        prepare_group<T, D, kChannelGate, G>(p, start + (int)g * kGroup, min(kGroup, end - start - (int)g * kGroup), h, lane, factor,
+                                             bias, sm.slot[slot], sm.m[slot]);
         if (lane == 0) bar_arrive(smem_u32(&sm.full[slot]));
     }
     return true;
@@ -502,7 +503,7 @@ bool few_pairs(const DeltaParams &p) { return (int64_t)p.num_seqs * p.heads < 2 
 
 template <typename T, int D, bool kChannelGate, typename G>
 struct Update {
-    static cudaError_t run(const DeltaParams &p, int, int *, kda_stream_t stream) {
+    static cudaError_t run(const DeltaParams &p, int, int, int *, kda_stream_t stream) {
         const unsigned pairs = (unsigned)((int64_t)p.num_seqs * p.heads);
         if (few_pairs(p))
             return launch(delta_update_kernel<T, D, 1, kChannelGate, G>, dim3(pairs, D / 32), kWarps * 32, 0, stream, p);
@@ -525,34 +526,36 @@ struct Recurrent {
         return launch(kernel, dim3((unsigned)(pairs < room ? pairs : room), kParts), (kRowWarps + kSlots) * 32, smem,
                       stream, p, min_len, max_len, head);
     }
-    static cudaError_t run(const DeltaParams &p, int max_len, int *head, kda_stream_t stream) {
+    static cudaError_t run(const DeltaParams &p, int min_len, int max_len, int *head, kda_stream_t stream) {
         // Two blocks of half the rows per pair while all pairs run at once.
-        if ((int64_t)p.num_seqs * p.heads * 2 <= current_sms()) return rows<D / 32, 6>(p, 1, max_len, head, stream);
-        return rows<D / 16, 4>(p, 1, max_len, head, stream);
+        if ((int64_t)p.num_seqs * p.heads * 2 <= current_sms()) return rows<D / 32, 4>(p, min_len, max_len, head, stream);
+        return rows<D / 16, 4>(p, min_len, max_len, head, stream);
     }
 };
 
 template <template <typename, int, bool, typename> class Op, typename T, int D>
-cudaError_t run_gate(const DeltaParams &p, bool channel, int max_len, int *head, kda_stream_t stream) {
-    if (!channel) return Op<T, D, false, float>::run(p, max_len, head, stream);
-    if (p.gate_dtype == KDA_DTYPE_F32) return Op<T, D, true, float>::run(p, max_len, head, stream);
-    if (p.gate_dtype == KDA_DTYPE_BF16) return Op<T, D, true, __nv_bfloat16>::run(p, max_len, head, stream);
-    return Op<T, D, true, __half>::run(p, max_len, head, stream);
+cudaError_t run_gate(const DeltaParams &p, bool channel, int min_len, int max_len, int *head, kda_stream_t stream) {
+    if (!channel) return Op<T, D, false, float>::run(p, min_len, max_len, head, stream);
+    if (p.gate_dtype == KDA_DTYPE_F32) return Op<T, D, true, float>::run(p, min_len, max_len, head, stream);
+    if (p.gate_dtype == KDA_DTYPE_BF16) return Op<T, D, true, __nv_bfloat16>::run(p, min_len, max_len, head, stream);
+    return Op<T, D, true, __half>::run(p, min_len, max_len, head, stream);
 }
 
 template <template <typename, int, bool, typename> class Op, typename T>
-cudaError_t run_dim(const DeltaParams &p, const kda_delta_t *d, int max_len, int *head, kda_stream_t stream) {
+cudaError_t run_dim(const DeltaParams &p, const kda_delta_t *d, int min_len, int max_len, int *head,
+                    kda_stream_t stream) {
     const bool channel = d->gate_per_channel != 0;
-    return d->head_dim == 64 ? run_gate<Op, T, 64>(p, channel, max_len, head, stream)
-                             : run_gate<Op, T, 128>(p, channel, max_len, head, stream);
+    return d->head_dim == 64 ? run_gate<Op, T, 64>(p, channel, min_len, max_len, head, stream)
+                             : run_gate<Op, T, 128>(p, channel, min_len, max_len, head, stream);
 }
 
-// Sequences of at most max_len tokens; head: 256 bytes to zero, or NULL.
+// Sequences of min_len to max_len tokens; head: 256 bytes to zero, or NULL.
 template <template <typename, int, bool, typename> class Op>
-cudaError_t run_op(const DeltaParams &p, const kda_delta_t *d, int max_len, int *head, kda_stream_t stream) {
-    if (d->x_dtype == KDA_DTYPE_BF16) return run_dim<Op, __nv_bfloat16>(p, d, max_len, head, stream);
-    if (d->x_dtype == KDA_DTYPE_F16) return run_dim<Op, __half>(p, d, max_len, head, stream);
-    return run_dim<Op, float>(p, d, max_len, head, stream);
+cudaError_t run_op(const DeltaParams &p, const kda_delta_t *d, int min_len, int max_len, int *head,
+                   kda_stream_t stream) {
+    if (d->x_dtype == KDA_DTYPE_BF16) return run_dim<Op, __nv_bfloat16>(p, d, min_len, max_len, head, stream);
+    if (d->x_dtype == KDA_DTYPE_F16) return run_dim<Op, __half>(p, d, min_len, max_len, head, stream);
+    return run_dim<Op, float>(p, d, min_len, max_len, head, stream);
 }
 
 bool strides_ok(const int64_t *s, int64_t quantum) {
@@ -609,14 +612,13 @@ DeltaParams params_of(const kda_delta_t *d) {
     return p;
 }
 
-// Sequences up to this length go four tokens at a time through FP32, longer ones in
-// chunks. Where all (sequence, head) pairs run at once (four blocks of 32 rows each,
-// two per SM) the chunked path's launches cost as much as about 80 tokens; a full
-// GPU does 40 tokens for the price of a chunk (bf16, 12 heads of 128, us: one
-// sequence of 64 tokens 22 against 33, of 128 42 against 36; 256 sequences of 32 362
-// against 494, of 64 682 against 507).
-int short_len(int64_t num_seqs, int64_t heads) {
-    return num_seqs * heads * 4 <= 2 * (int64_t)current_sms() ? 80 : 40;
+// Sequences up to this length go in groups of eight tokens, longer ones in chunks.
+// While all (sequence, head) pairs run at once, a group costs 1 us and the chunked
+// path's launches 35 us; a full GPU does about 70 tokens for the price of a chunk
+// (bf16, 12 heads of 128, us: one sequence of 96 tokens 27 against 38, of 192 49
+// against 41; 64 sequences of 64 150 against 161, of 128 288 against 254).
+int short_len(int64_t num_seqs, int64_t heads, int sms) {
+    return num_seqs * heads * 2 <= (int64_t)sms ? 112 : 72;
 }
 
 // Whether a packed call uses the chunked path: 16-bit x and sequences that can be long.
@@ -644,8 +646,11 @@ kda_status_t kda_packed_delta_rule_workspace(int64_t tokens, int64_t num_seqs, i
         return KDA_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return KDA_ERR_UNSUPPORTED;
     *bytes = 0;
-    if (tokens > 0 && num_seqs > 0 && uses_chunks(tokens, x_dtype, 40))  // the shorter of the two lengths
-        *bytes = chunk_plan(tokens, num_seqs, heads, head_dim, sm_count ? sm_count : current_sms()).bytes;
+    if (tokens > 0 && num_seqs > 0) {
+        const int sms = sm_count ? sm_count : current_sms(), short_tokens = short_len(num_seqs, heads, sms);
+        if (uses_chunks(tokens, x_dtype, short_tokens))
+            *bytes = chunk_plan(tokens, num_seqs, heads, head_dim, short_tokens, sms).bytes;
+    }
     return KDA_OK;
 }
 
@@ -666,14 +671,25 @@ kda_status_t kda_packed_delta_rule(const kda_delta_t *d, int64_t tokens,
     p.null_block_id = null_block_id;
     p.num_seqs = (int)num_seqs;
     p.tokens = tokens;
-    const int short_tokens = short_len(num_seqs, d->heads);
-    if (!uses_chunks(tokens, d->x_dtype, short_tokens)) return cuda_status(run_op<Recurrent>(p, d, INT32_MAX, nullptr, stream));
-    const ChunkPlan plan = chunk_plan(tokens, num_seqs, d->heads, d->head_dim, current_sms());
+    const int sms = current_sms(), short_tokens = short_len(num_seqs, d->heads, sms);
+    // One-token sequences among many (decode tokens in a prefill batch) are the update's:
+    // bound by their states' bytes, which the groups' pipeline does not stream as fast.
+    const bool apart = num_seqs * d->heads * 2 > sms && tokens < 32 * num_seqs;
+    const int min_len = apart ? 2 : 1;
+    if (!uses_chunks(tokens, d->x_dtype, short_tokens)) {
+        cudaError_t e = cudaSuccess;
+        if (apart) e = run_op<Update>(p, d, 1, 1, nullptr, stream);
+        if (e == cudaSuccess) e = run_op<Recurrent>(p, d, min_len, INT32_MAX, nullptr, stream);
+        return cuda_status(e);
+    }
+    const ChunkPlan plan = chunk_plan(tokens, num_seqs, d->heads, d->head_dim, short_tokens, sms);
     if (workspace == nullptr || workspace_bytes < plan.bytes || plan.slots * d->heads > INT32_MAX)
         return KDA_ERR_INVALID_ARG;
     if (!aligned(workspace, 256)) return KDA_ERR_MISALIGNED;
     // The short sequences first: that kernel also zeroes the workspace's head.
-    cudaError_t e = run_op<Recurrent>(p, d, short_tokens, static_cast<int *>(workspace), stream);
+    cudaError_t e = cudaSuccess;
+    if (apart) e = run_op<Update>(p, d, 1, 1, nullptr, stream);
+    if (e == cudaSuccess) e = run_op<Recurrent>(p, d, min_len, short_tokens, static_cast<int *>(workspace), stream);
     if (e == cudaSuccess) e = run_chunked(p, d, plan, short_tokens, workspace, stream);
     return cuda_status(e);
 }
@@ -690,7 +706,7 @@ kda_status_t kda_delta_rule_update(const kda_delta_t *d, int64_t batch, const in
     p.null_block_id = null_block_id;
     p.num_seqs = (int)batch;
     p.tokens = batch;
-    return cuda_status(run_op<Update>(p, d, 1, nullptr, stream));
+    return cuda_status(run_op<Update>(p, d, 1, 1, nullptr, stream));
 }
 
 }  // extern "C"

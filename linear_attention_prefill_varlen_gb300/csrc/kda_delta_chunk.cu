@@ -77,6 +77,7 @@ struct WalkArgs {
     float *start;          // [segment slot][head][D][D]: the state a segment starts from
     int64_t seg_tokens;    // tokens of a segment (a multiple of 64)
     int short_len;
+    int by_start;          // the form of first_slot
 };
 
 __host__ __device__ constexpr int64_t slot_bytes(int D) { return D == 64 ? Slot<64>::bytes : Slot<128>::bytes; }
@@ -172,21 +173,37 @@ __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t byt
 
 // ------------------------------------------------------------------ prepare
 
-// The sequence that owns chunk slot j: the largest s with f(s) <= j for f(s) =
-// floor(qsl[s] / 64) + s; rest = j - f(s), the chunk's number in it. By a whole block
-// of 256 threads: each round narrows the range 256-fold with one load per thread.
-__device__ __forceinline__ int find_seq_block(const DeltaParams &p, int64_t j, int64_t &rest) {
+// The first chunk slot of sequence s, whose tokens start at row `start`: floor(start /
+// 64) + s, or, for batches of many short sequences, floor(start / 64) + ceil(start /
+// (short_len + 1)). Only sequences of more than short_len tokens use slots; the next
+// of them starts more than short_len rows on, which moves the second term by one or
+// more, so neither form gives a slot twice, and the second does not grow with the
+// number of sequences.
+__device__ __forceinline__ int first_slot(const WalkArgs &w, int start, int s) {
+    return start / kChunk + (w.by_start ? (start + w.short_len) / (w.short_len + 1) : s);
+}
+
+// The sequence that owns chunk slot j: the last whose first slot is at most j; rest =
+// the chunk's number in it. By a whole block of 256 threads: each round narrows the
+// range 256-fold with one load per thread.
+__device__ __forceinline__ int find_seq_block(const DeltaParams &p, const WalkArgs &w, int j, int64_t &rest) {
     int lo = 0, n = p.num_seqs;
     while (n > 1) {
         const int step = (n + 255) / 256, i = (int)threadIdx.x * step;
         bool below = false;
-        if (i < n) below = max(p.query_start_loc[lo + i], 0) / kChunk + lo + i <= j;
+        if (i < n) below = first_slot(w, max(p.query_start_loc[lo + i], 0), lo + i) <= j;
         const int count = max(__syncthreads_count(below), 1);
         lo += (count - 1) * step;
         n = min(step, n - (count - 1) * step);
     }
-    rest = j - (max(p.query_start_loc[lo], 0) / kChunk + lo);
+    rest = j - first_slot(w, max(p.query_start_loc[lo], 0), lo);
     return lo;
+}
+
+// The first segment slot of a sequence of several segments (by the same argument:
+// more than seg_tokens rows lie between two of them).
+__device__ __forceinline__ int64_t first_segment(const WalkArgs &w, int64_t start) {
+    return (start + w.seg_tokens - 1) / w.seg_tokens + (start + w.seg_tokens) / (w.seg_tokens + 1);
 }
 
 template <int D>
@@ -305,7 +322,7 @@ __global__ void __launch_bounds__(256, 2)
     const int64_t slot = blockIdx.x / p.heads;
     const int h = blockIdx.x % p.heads;
     int64_t chunk;
-    const int s = find_seq_block(p, slot, chunk);
+    const int s = find_seq_block(p, w, (int)slot, chunk);
     const Seq seq = load_seq(p, s);
     const int64_t len = seq.end - seq.start;
     if (len <= w.short_len || chunk < 0 || chunk * kChunk >= len) return;
@@ -320,7 +337,7 @@ __global__ void __launch_bounds__(256, 2)
         g.begin = (int)t0;
         g.rows = (int)(last ? seq.end - t0 : w.seg_tokens);
         g.slot = (int)slot;
-        g.at = (int)(seq.start / w.seg_tokens + s + seg);
+        g.at = (int)(first_segment(w, seq.start) + seg);  // used where there are several
         g.line = (int)seq.line;
         g.first = seg == 0, g.last = last, g.reads = seq.reads;
         // At most one entry per chunk slot, so the lists cannot run over.
@@ -1527,7 +1544,7 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
     const int64_t len = seq.end - seq.start;
     if (t < seq.start || t - seq.start >= w.seg_tokens || len <= w.short_len || len <= w.seg_tokens) return;
     const int segs = (int)((len + w.seg_tokens - 1) / w.seg_tokens);
-    const int64_t base = seq.start / w.seg_tokens + lo;
+    const int64_t base = first_segment(w, seq.start);
     const int tid = threadIdx.x, k = tid % D, r0 = tid / D * kOwn, row0 = blockIdx.z * kJoinRows + r0;
     // In the product: 4 columns, 8 rows and one part of the sum.
     const int c4 = tid % (D / 4) * 4, r8 = tid / (D / 4) % 2 * 8, split = tid / (D / 4) / 2;
@@ -1652,6 +1669,7 @@ cudaError_t run(const DeltaParams &p, const kda_delta_t *d, const ChunkPlan &pla
     w.ws = ws;
     w.seg_tokens = (int64_t)plan.seg_chunks * kChunk;
     w.short_len = short_len;
+    w.by_start = plan.by_start;
     w.full = reinterpret_cast<Segment *>(ws + kHeader + plan.slots * p.heads * slot_bytes(D));
     w.tail = w.full + plan.slots;
     cudaError_t e;
@@ -1674,14 +1692,16 @@ cudaError_t run(const DeltaParams &p, const kda_delta_t *d, const ChunkPlan &pla
                    stream, p, w);
         if (e != cudaSuccess) return e;
     }
-    return launch_walk<T, D, kWalkOut>(p, w, (plan.split ? plan.segments : p.num_seqs) * p.heads, stream);
+    return launch_walk<T, D, kWalkOut>(p, w, plan.slots * p.heads, stream);
 }
 
 }  // namespace
 
-ChunkPlan chunk_plan(int64_t tokens, int64_t num_seqs, int64_t heads, int head_dim, int sms) {
+ChunkPlan chunk_plan(int64_t tokens, int64_t num_seqs, int64_t heads, int head_dim, int short_len, int sms) {
     ChunkPlan c = {};
-    c.slots = tokens / kChunk + num_seqs;
+    const int64_t by_start = tokens / (short_len + 1) + 2;
+    c.by_start = by_start < num_seqs;
+    c.slots = tokens / kChunk + (c.by_start ? by_start : num_seqs);
     const int64_t chunks = (tokens + kChunk - 1) / kChunk;  // of one sequence, at most
     // One wave of segments if one sequence had all tokens, of at least 8 chunks: a split
     // sequence is walked twice and pays the join.
@@ -1691,7 +1711,7 @@ ChunkPlan chunk_plan(int64_t tokens, int64_t num_seqs, int64_t heads, int head_d
     c.split = chunks > 16 && chunks > seg;
     if (!c.split) seg = chunks > 0 ? chunks : 1;
     c.seg_chunks = (int)seg;
-    c.segments = c.split ? tokens / (seg * kChunk) + num_seqs : num_seqs;
+    c.segments = 2 * (tokens / (seg * kChunk)) + 4;
     c.bytes = kHeader + c.slots * heads * slot_bytes(head_dim) + 2 * c.slots * (int64_t)sizeof(Segment);
     if (c.split) c.bytes += c.segments * heads * 3 * head_dim * head_dim * 4;
     return c;

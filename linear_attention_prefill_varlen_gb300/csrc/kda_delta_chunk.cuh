@@ -10,14 +10,15 @@ constexpr int kChunk = 64;  // tokens of a chunk
 // How a packed batch is cut: chunks of 64 tokens inside each sequence, and
 // segments of seg_chunks chunks that are walked by different blocks.
 struct ChunkPlan {
-    int64_t slots;       // chunk slots: floor(tokens / 64) + num_seqs
-    int64_t segments;    // segment slots: floor(tokens / (64 seg_chunks)) + num_seqs
+    int64_t slots;       // chunk slots: at most these are used (first_slot)
+    int64_t segments;    // segment slots of sequences of several segments (first_segment)
+    int by_start;        // how sequences are given slots
     int seg_chunks;
     bool split;          // whether a sequence can have more than one segment
     int64_t bytes;       // workspace
 };
 
-ChunkPlan chunk_plan(int64_t tokens, int64_t num_seqs, int64_t heads, int head_dim, int sms);
+ChunkPlan chunk_plan(int64_t tokens, int64_t num_seqs, int64_t heads, int head_dim, int short_len, int sms);
 
 // Sequences of more than short_len tokens, x of 16 bits. ws: plan.bytes, 256-byte aligned.
 cudaError_t run_chunked(const DeltaParams &p, const kda_delta_t *d, const ChunkPlan &plan,
