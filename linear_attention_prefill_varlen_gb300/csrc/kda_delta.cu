@@ -614,11 +614,12 @@ DeltaParams params_of(const kda_delta_t *d) {
 
 // Sequences up to this length go in groups of eight tokens, longer ones in chunks.
 // While all (sequence, head) pairs run at once, a group costs 1 us and the chunked
-// path's launches 35 us; a full GPU does about 70 tokens for the price of a chunk
-// (bf16, 12 heads of 128, us: one sequence of 96 tokens 27 against 38, of 192 49
-// against 41; 64 sequences of 64 150 against 161, of 128 288 against 254).
+// path's launches 35 us; on a full GPU a group costs a seventh of a chunk (bf16, 12
+// heads of 128, us, groups against chunks: one sequence of 96 tokens 24 against 38,
+// of 192 43 against 41; 256 sequences of 32 297 against 495, of 64 548 against 500;
+// 256 sequences of 1 to 128 among 1024 of one 893 with 32 here, 965 with 72).
 int short_len(int64_t num_seqs, int64_t heads, int sms) {
-    return num_seqs * heads * 2 <= (int64_t)sms ? 112 : 72;
+    return num_seqs * heads * 2 <= (int64_t)sms ? 112 : 32;
 }
 
 // Whether a packed call uses the chunked path: 16-bit x and sequences that can be long.

@@ -468,6 +468,7 @@ __global__ void __launch_bounds__(256, 2)
     const float down_kk = down_k * down_k;
 
     const int g = lane / 4, cc = lane % 4 * 2;
+    constexpr bool kFine = std::is_same<T, __half>::value;
     constexpr int kRow = PrepSmem<D>::kRow;
     if constexpr (kChannelGate) {
     // ---- pairs inside 8 tokens: running products of decays, FP32. For i = 0..7: q_i k_i,
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(256, 2)
             }
         }
         __syncthreads();
-        // kk by hi hi + hi lo + lo hi, qk by hi hi
+        // kk by hi hi + hi lo + lo hi, qk by hi hi (and hi lo where o has 11 bits)
         if (half == 1) {
             if (b < 4) {  // pair b: rows of k in the tile's first 8 rows, of q in the others
                 float c[4] = {}, c1[4] = {}, c2[4] = {};
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__(256, 2)
                     al[1] = al[3] = 0;
                     mma16(c, ah, bh);
                     mma16(c1, al, bh);
-                    ah[1] = ah[3] = 0;
+                    if (!kFine) ah[1] = ah[3] = 0;
                     mma16(c2, ah, bl);
                 }
                 const int i = b * 16 + 8 + g, j = b * 16 + cc;
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     sm.l.L[i][j + e] = (c[e] + (c1[e] + c2[e])) * f;
-                    sm.A[i][j + e] = __float2half_rn(c[2 + e] * kDownA);
+                    sm.A[i][j + e] = __float2half_rn((kFine ? c[2 + e] + c2[2 + e] : c[2 + e]) * kDownA);
                 }
             }
         } else {
@@ -590,11 +591,12 @@ __global__ void __launch_bounds__(256, 2)
             for (int kk = 0; kk < D; kk += 16) {
                 uint32_t ah[4], bh[2];
                 ldsm2(bh, right + kk * 2);
+                uint32_t bl[2];
+                if (do_k || kFine) ldsm2(bl, right + kPlane + kk * 2);
                 if (do_k) {
-                    uint32_t al[4], bl[2];
+                    uint32_t al[4];
                     ldsm4(ah, at_lk + left + kk * 2);
                     ldsm4(al, at_lk + kPlane + left + kk * 2);
-                    ldsm2(bl, right + kPlane + kk * 2);
                     mma16(ck, ah, bh);
                     mma16(ck1, al, bh);
                     mma16(ck2, ah, bl);
@@ -602,6 +604,7 @@ __global__ void __launch_bounds__(256, 2)
                 if (do_q) {
                     ldsm4(ah, at_lq + left + kk * 2);
                     mma16(cq, ah, bh);
+                    if (kFine) mma16(cq, ah, bl);
                 }
             }
             // token rows and columns of the tile
