@@ -73,10 +73,7 @@ def _check(status: int) -> None:
         raise KdaError(status, what)
 
 
-def _raw_stream(stream, index: int) -> int:
-    """The raw handle: `stream`, or torch's current stream of device `index`."""
-    if stream is None:
-        return _current_raw_stream(index)
+def _raw_stream(stream) -> int:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -85,26 +82,14 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-class _Here:
-    """A context that does nothing: the tensors' device is the current one already."""
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *_):
-        return None
-
-
-_here = _Here()
-
-
-def _on_device(index: int):
-    return _here if torch.cuda.current_device() == index else torch.cuda.device(index)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _empty_like(t: torch.Tensor, stream) -> torch.Tensor:
     """A contiguous tensor of t's shape and type for a call on `stream`."""
-    return t.new_empty(t.shape) if stream is None else _empty_on(stream, t.shape, t.dtype, t.device)
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return _empty_on(stream, t.shape, t.dtype, t.device)
 
 
 def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
@@ -258,7 +243,7 @@ def delta_rule_workspace(tokens: int, num_seqs: int, heads: int, head_dim: int,
     """Bytes of workspace packed_delta_rule_fn uses for these sizes (sm_count 0:
     the current device)."""
     n = _I64()
-    _check(_lib().kda_packed_delta_rule_workspace(tokens, num_seqs, heads, head_dim,
+    _check((_declared or _lib()).kda_packed_delta_rule_workspace(tokens, num_seqs, heads, head_dim,
                                                   _DTYPES[dtype], sm_count, ctypes.byref(n)))
     return n.value
 
@@ -296,22 +281,27 @@ def packed_delta_rule_fn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate
                        {"query_start_loc": query_start_loc, "cache_indices": cache_indices,
                         "has_initial_state": has_initial_state})
     tokens, heads, dim = q.shape
-    with _on_device(index):
-        if out is None:
-            out = _empty_like(q, stream)
-        need = delta_rule_workspace(tokens, num_seqs, heads, dim, q.dtype)
-        if workspace is None:
-            if need:
-                workspace = _empty_on(stream, (need,), torch.uint8, q.device)
-        elif (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
-              or workspace.get_device() != index):
-            raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-        _check(_lib().kda_packed_delta_rule(
-            _delta(q, k, v, gate, beta, states, scale, a_log, dt_bias, beta_logits, out,
-                   cache_indices), tokens, cache_indices.data_ptr(),
-            has_initial_state.data_ptr(), query_start_loc.data_ptr(), num_seqs,
-            _null(null_block_id), _ptr(workspace),
-            0 if workspace is None else workspace.numel(), _raw_stream(stream, index)))
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return packed_delta_rule_fn(
+                q, k, v, gate, beta, states, query_start_loc, cache_indices, has_initial_state,
+                scale, a_log, dt_bias, beta_logits, null_block_id, out, workspace, stream)
+    if out is None:
+        out = _empty_like(q, stream)
+    need = delta_rule_workspace(tokens, num_seqs, heads, dim, q.dtype)
+    if workspace is None:
+        if need:
+            workspace = _empty_on(stream, (need,), torch.uint8, q.device)
+    elif (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
+          or workspace.get_device() != index):
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    _check((_declared or _lib()).kda_packed_delta_rule(
+        _delta(q, k, v, gate, beta, states, scale, a_log, dt_bias, beta_logits, out,
+               cache_indices), tokens, cache_indices.data_ptr(),
+        has_initial_state.data_ptr(), query_start_loc.data_ptr(), num_seqs,
+        _null(null_block_id), _ptr(workspace),
+        0 if workspace is None else workspace.numel(),
+        _current_raw_stream(index) if stream is None else _raw_stream(stream)))
     return out
 
 
@@ -328,13 +318,16 @@ def delta_rule_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate: t
     if not _delta_ok(q, k, v, gate, beta, states, a_log, dt_bias, out, cache_indices, batch):
         _explain_delta(q, k, v, gate, beta, states, a_log, dt_bias, out,
                        {"cache_indices": cache_indices})
-    with _on_device(index):
-        if out is None:
-            out = _empty_like(q, stream)
-        _check(_lib().kda_delta_rule_update(
-            _delta(q, k, v, gate, beta, states, scale, a_log, dt_bias, beta_logits, out,
-                   cache_indices), batch, cache_indices.data_ptr(), _null(null_block_id),
-            _raw_stream(stream, index)))
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return delta_rule_update(q, k, v, gate, beta, states, cache_indices, scale, a_log,
+                                     dt_bias, beta_logits, null_block_id, out, stream)
+    if out is None:
+        out = _empty_like(q, stream)
+    _check((_declared or _lib()).kda_delta_rule_update(
+        _delta(q, k, v, gate, beta, states, scale, a_log, dt_bias, beta_logits, out,
+               cache_indices), batch, cache_indices.data_ptr(), _null(null_block_id),
+        _current_raw_stream(index) if stream is None else _raw_stream(stream)))
     return out
 
 
@@ -388,20 +381,23 @@ def gated_rmsnorm(x: torch.Tensor, gate: torch.Tensor | None, weight: torch.Tens
         _written("out", out)
         _vector32("weight", weight, [(x.size(2),)])
         _same_device("x", x=x, gate=gate, weight=weight, out=out)
-    with _on_device(index):
-        if out is None:
-            out = _empty_like(x, stream)
-        g = x if gate is None else gate
-        pairs = _SixLong(*x.stride()[:2], *g.stride()[:2], *out.stride()[:2])
-        if shape[0] <= 1:  # the stride of an axis of one entry is never used
-            pairs[0] = pairs[2] = pairs[4] = 0
-        if shape[1] == 1:
-            pairs[1] = pairs[3] = pairs[5] = 0
-        at = ctypes.addressof(pairs)
-        _check(_lib().kda_gated_rmsnorm(
-            x.data_ptr(), at, None if gate is None else gate.data_ptr(), at + 16, _ptr(weight),
-            eps, act, shape[0], shape[1], shape[2], _DTYPES[dt], out.data_ptr(), at + 32,
-            _raw_stream(stream, index)))
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return gated_rmsnorm(x, gate, weight, eps, activation, out, stream)
+    if out is None:
+        out = _empty_like(x, stream)
+    g = x if gate is None else gate
+    pairs = _SixLong(*x.stride()[:2], *g.stride()[:2], *out.stride()[:2])
+    if shape[0] <= 1:  # the stride of an axis of one entry is never used
+        pairs[0] = pairs[2] = pairs[4] = 0
+    if shape[1] == 1:
+        pairs[1] = pairs[3] = pairs[5] = 0
+    at = ctypes.addressof(pairs)
+    _check((_declared or _lib()).kda_gated_rmsnorm(
+        x.data_ptr(), at, None if gate is None else gate.data_ptr(), at + 16,
+        None if weight is None else weight.data_ptr(),
+        eps, act, shape[0], shape[1], shape[2], _DTYPES[dt], out.data_ptr(), at + 32,
+        _current_raw_stream(index) if stream is None else _raw_stream(stream)))
     return out
 
 
@@ -448,16 +444,20 @@ def residual_rmsnorm(y: torch.Tensor, residual: torch.Tensor, weight: torch.Tens
                      post_weight=post_weight, out=out, residual_out=residual_out)
     rows, width = shape
     many = rows > 1  # the stride of an axis of one entry is never used
-    with _on_device(index):
-        if out is None:
-            out = _empty_like(y, stream)
-        if residual_out is None:
-            residual_out = residual
-        _check(_lib().kda_residual_rmsnorm(
-            y.data_ptr(), y.stride(0) if many else 0, residual.data_ptr(),
-            residual.stride(0) if many else 0, _ptr(gate),
-            gate.stride(0) if many and gate is not None else 0, _ptr(weight), _ptr(post_weight),
-            scale, eps, act, rows, width, _DTYPES[dt], 1 if rt is torch.float32 else 0,
-            out.data_ptr(), out.stride(0) if many else 0, residual_out.data_ptr(),
-            residual_out.stride(0) if many else 0, _raw_stream(stream, index)))
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return residual_rmsnorm(y, residual, weight, scale, gate, activation, post_weight,
+                                    eps, out, residual_out, stream)
+    if out is None:
+        out = _empty_like(y, stream)
+    if residual_out is None:
+        residual_out = residual
+    _check((_declared or _lib()).kda_residual_rmsnorm(
+        y.data_ptr(), y.stride(0) if many else 0, residual.data_ptr(),
+        residual.stride(0) if many else 0, _ptr(gate),
+        gate.stride(0) if many and gate is not None else 0, _ptr(weight), _ptr(post_weight),
+        scale, eps, act, rows, width, _DTYPES[dt], 1 if rt is torch.float32 else 0,
+        out.data_ptr(), out.stride(0) if many else 0, residual_out.data_ptr(),
+        residual_out.stride(0) if many else 0,
+        _current_raw_stream(index) if stream is None else _raw_stream(stream)))
     return out, residual_out

@@ -471,211 +471,211 @@ __global__ void __launch_bounds__(256, 2)
     constexpr bool kFine = std::is_same<T, __half>::value;
     constexpr int kRow = PrepSmem<D>::kRow;
     if constexpr (kChannelGate) {
-    // ---- pairs inside 8 tokens: running products of decays, FP32. For i = 0..7: q_i k_i,
-    // then for j < i the pair (k_i k_j, q_i k_j); 64 sums in batches of 16.
-    {
-        repack(k), repack(q);
-        float f[16];
-        float2 w[8][P];  // k_j decayed to token i
+        // ---- pairs inside 8 tokens: running products of decays, FP32. For i = 0..7: q_i k_i,
+        // then for j < i the pair (k_i k_j, q_i k_j); 64 sums in batches of 16.
+        {
+            repack(k), repack(q);
+            float f[16];
+            float2 w[8][P];  // k_j decayed to token i
 #pragma unroll
-        for (int ii = 0; ii < 8; ++ii) {
-            float2 ki[P], qi[P];
-#pragma unroll
-            for (int c = 0; c < P; ++c) {
-                ki[c] = __half22float2(k[ii][c]), qi[c] = __half22float2(q[ii][c]);
-                w[ii][c] = ki[c];
-            }
-#pragma unroll
-            for (int e = 0; e <= 2 * ii; ++e) {  // 0: q_i k_i, 1 + 2 j: k_i k_j, 2 + 2 j: q_i k_j
-                const int jj = e == 0 ? ii : (e - 1) / 2;
-                const bool of_k = e % 2 == 1;
-                float2 sum;
+            for (int ii = 0; ii < 8; ++ii) {
+                float2 ki[P], qi[P];
 #pragma unroll
                 for (int c = 0; c < P; ++c) {
-                    if (of_k) w[jj][c] = mul2(w[jj][c], a[ii][c]);
-                    const float2 x = of_k ? ki[c] : qi[c];
-                    sum = c == 0 ? mul2(x, w[jj][c]) : fma2(x, w[jj][c], sum);
+                    ki[c] = __half22float2(k[ii][c]), qi[c] = __half22float2(q[ii][c]);
+                    w[ii][c] = ki[c];
                 }
-                const int at = ii * ii + e;
-                f[at % 16] = sum.x + sum.y;
-                if (at % 16 == 15) {
-                    const float got = scatter_sum(f, lane);
-                    const int mine = at - 15 + lane / 2;
-                    const int i = (mine >= 1) + (mine >= 4) + (mine >= 9) + (mine >= 16) + (mine >= 25) + (mine >= 36) + (mine >= 49);
-                    const int own = mine - i * i, j = own == 0 ? i : (own - 1) / 2;
-                    if (own % 2 == 1) sm.l.L[b * 8 + i][b * 8 + j] = got * down_kk * sm.beta[b * 8 + i];
-                    else sm.A[b * 8 + i][b * 8 + j] = __float2half_rn(got * kDownA);
+#pragma unroll
+                for (int e = 0; e <= 2 * ii; ++e) {  // 0: q_i k_i, 1 + 2 j: k_i k_j, 2 + 2 j: q_i k_j
+                    const int jj = e == 0 ? ii : (e - 1) / 2;
+                    const bool of_k = e % 2 == 1;
+                    float2 sum;
+#pragma unroll
+                    for (int c = 0; c < P; ++c) {
+                        if (of_k) w[jj][c] = mul2(w[jj][c], a[ii][c]);
+                        const float2 x = of_k ? ki[c] : qi[c];
+                        sum = c == 0 ? mul2(x, w[jj][c]) : fma2(x, w[jj][c], sum);
+                    }
+                    const int at = ii * ii + e;
+                    f[at % 16] = sum.x + sum.y;
+                    if (at % 16 == 15) {
+                        const float got = scatter_sum(f, lane);
+                        const int mine = at - 15 + lane / 2;
+                        const int i = (mine >= 1) + (mine >= 4) + (mine >= 9) + (mine >= 16) + (mine >= 25) + (mine >= 36) + (mine >= 49);
+                        const int own = mine - i * i, j = own == 0 ? i : (own - 1) / 2;
+                        if (own % 2 == 1) sm.l.L[b * 8 + i][b * 8 + j] = got * down_kk * sm.beta[b * 8 + i];
+                        else sm.A[b * 8 + i][b * 8 + j] = __float2half_rn(got * kDownA);
+                    }
                 }
             }
         }
-    }
 
-    // ---- pairs of blocks: per level, the later half's tokens carry the decays
-    // from the middle to them, the earlier half's those from them to the middle
-    constexpr int kPlane = 32 * kRow * 2;  // bytes from hi to lo
-    const uint32_t at_lk = smem_u32(sm.x.lv.lk_hi), at_lq = smem_u32(sm.x.lv.lq), at_rk = smem_u32(sm.x.lv.rk_hi);
+        // ---- pairs of blocks: per level, the later half's tokens carry the decays
+        // from the middle to them, the earlier half's those from them to the middle
+        constexpr int kPlane = 32 * kRow * 2;  // bytes from hi to lo
+        const uint32_t at_lk = smem_u32(sm.x.lv.lk_hi), at_lq = smem_u32(sm.x.lv.lq), at_rk = smem_u32(sm.x.lv.rk_hi);
 #pragma unroll 1
-    for (int half = 1; half <= 4; half *= 2) {  // blocks of 8 in half a level: 1, 2, 4
-        repack(k), repack(q);
-        const int pos = b % (2 * half);         // block's place in its level group
-        const int row0 = b / (2 * half) * (half * 8) + (pos % half) * 8;
-        float2 run[P];
+        for (int half = 1; half <= 4; half *= 2) {  // blocks of 8 in half a level: 1, 2, 4
+            repack(k), repack(q);
+            const int pos = b % (2 * half);         // block's place in its level group
+            const int row0 = b / (2 * half) * (half * 8) + (pos % half) * 8;
+            float2 run[P];
 #pragma unroll
-        for (int c = 0; c < P; ++c) run[c] = make_float2(1.0f, 1.0f);
-        const bool later = pos >= half;
-        for (int o = later ? half : pos + 1; o < (later ? pos : half); ++o)
+            for (int c = 0; c < P; ++c) run[c] = make_float2(1.0f, 1.0f);
+            const bool later = pos >= half;
+            for (int o = later ? half : pos + 1; o < (later ? pos : half); ++o)
 #pragma unroll
-            for (int c = 0; c < P; ++c)
-                run[c] = mul2(run[c], *reinterpret_cast<const float2 *>(&sm.block_decay[b - pos + o][lane * C + 2 * c]));
-        if (later) {
+                for (int c = 0; c < P; ++c)
+                    run[c] = mul2(run[c], *reinterpret_cast<const float2 *>(&sm.block_decay[b - pos + o][lane * C + 2 * c]));
+            if (later) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                float2 f[P], fq[P];
+                for (int r = 0; r < 8; ++r) {
+                    float2 f[P], fq[P];
 #pragma unroll
-                for (int c = 0; c < P; ++c) {
-                    run[c] = mul2(run[c], a[r][c]);
-                    f[c] = mul2(__half22float2(k[r][c]), run[c]);
-                    fq[c] = mul2(__half22float2(q[r][c]), run[c]);
+                    for (int c = 0; c < P; ++c) {
+                        run[c] = mul2(run[c], a[r][c]);
+                        f[c] = mul2(__half22float2(k[r][c]), run[c]);
+                        fq[c] = mul2(__half22float2(q[r][c]), run[c]);
+                    }
+                    store_split<P>(&sm.x.lv.lk_hi[row0 + r][lane * C], &sm.x.lv.lk_lo[row0 + r][lane * C], f);
+                    store_row<P>(&sm.x.lv.lq[row0 + r][lane * C], fq);
                 }
-                store_split<P>(&sm.x.lv.lk_hi[row0 + r][lane * C], &sm.x.lv.lk_lo[row0 + r][lane * C], f);
-                store_row<P>(&sm.x.lv.lq[row0 + r][lane * C], fq);
-            }
-        } else {
+            } else {
 #pragma unroll
-            for (int r = 7; r >= 0; --r) {
-                float2 f[P];
+                for (int r = 7; r >= 0; --r) {
+                    float2 f[P];
 #pragma unroll
-                for (int c = 0; c < P; ++c) f[c] = mul2(__half22float2(k[r][c]), run[c]), run[c] = mul2(run[c], a[r][c]);
-                store_split<P>(&sm.x.lv.rk_hi[row0 + r][lane * C], &sm.x.lv.rk_lo[row0 + r][lane * C], f);
+                    for (int c = 0; c < P; ++c) f[c] = mul2(__half22float2(k[r][c]), run[c]), run[c] = mul2(run[c], a[r][c]);
+                    store_split<P>(&sm.x.lv.rk_hi[row0 + r][lane * C], &sm.x.lv.rk_lo[row0 + r][lane * C], f);
+                }
             }
-        }
-        __syncthreads();
-        // kk by hi hi + hi lo + lo hi, qk by hi hi (and hi lo where o has 11 bits)
-        if (half == 1) {
-            if (b < 4) {  // pair b: rows of k in the tile's first 8 rows, of q in the others
-                float c[4] = {}, c1[4] = {}, c2[4] = {};
-                const int lr = lane % 8, piece = lane / 8;
-                const uint32_t left = (uint32_t)((b * 8 + lr) * kRow + (piece >> 1) * 8) * 2;
-                const uint32_t top = left + ((piece & 1) ? at_lq : at_lk), low = left + at_lk + kPlane;
-                const uint32_t right = at_rk + (uint32_t)((b * 8 + lane % 8) * kRow + (lane / 8 % 2) * 8) * 2;
+            __syncthreads();
+            // kk by hi hi + hi lo + lo hi, qk by hi hi (and hi lo where o has 11 bits)
+            if (half == 1) {
+                if (b < 4) {  // pair b: rows of k in the tile's first 8 rows, of q in the others
+                    float c[4] = {}, c1[4] = {}, c2[4] = {};
+                    const int lr = lane % 8, piece = lane / 8;
+                    const uint32_t left = (uint32_t)((b * 8 + lr) * kRow + (piece >> 1) * 8) * 2;
+                    const uint32_t top = left + ((piece & 1) ? at_lq : at_lk), low = left + at_lk + kPlane;
+                    const uint32_t right = at_rk + (uint32_t)((b * 8 + lane % 8) * kRow + (lane / 8 % 2) * 8) * 2;
+#pragma unroll
+                    for (int kk = 0; kk < D; kk += 16) {
+                        uint32_t ah[4], al[4], bh[2], bl[2];
+                        ldsm4(ah, top + kk * 2);
+                        ldsm4(al, low + kk * 2);
+                        ldsm2(bh, right + kk * 2);
+                        ldsm2(bl, right + kPlane + kk * 2);
+                        al[1] = al[3] = 0;
+                        mma16(c, ah, bh);
+                        mma16(c1, al, bh);
+                        if (!kFine) ah[1] = ah[3] = 0;
+                        mma16(c2, ah, bl);
+                    }
+                    const int i = b * 16 + 8 + g, j = b * 16 + cc;
+                    const float f = sm.beta[i] * down_kk;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        sm.l.L[i][j + e] = (c[e] + (c1[e] + c2[e])) * f;
+                        sm.A[i][j + e] = __float2half_rn((kFine ? c[2 + e] + c2[2 + e] : c[2 + e]) * kDownA);
+                    }
+                }
+            } else {
+                const bool wide = half == 4;
+                const int m = b / 4;                              // 16-row tile of the left operand
+                const int nt = wide ? b % 4 : m * 2 + b / 2 % 2;  // 8-row tile of the right operand
+                const bool do_k = wide || b % 2 == 0, do_q = wide || b % 2 == 1;
+                float ck[4] = {}, ck1[4] = {}, ck2[4] = {}, cq[4] = {};
+                const uint32_t left = (uint32_t)((m * 16 + lane % 16) * kRow + lane / 16 * 8) * 2;
+                const uint32_t right = at_rk + (uint32_t)((nt * 8 + lane % 8) * kRow + (lane / 8 % 2) * 8) * 2;
 #pragma unroll
                 for (int kk = 0; kk < D; kk += 16) {
-                    uint32_t ah[4], al[4], bh[2], bl[2];
-                    ldsm4(ah, top + kk * 2);
-                    ldsm4(al, low + kk * 2);
+                    uint32_t ah[4], bh[2];
                     ldsm2(bh, right + kk * 2);
-                    ldsm2(bl, right + kPlane + kk * 2);
-                    al[1] = al[3] = 0;
-                    mma16(c, ah, bh);
-                    mma16(c1, al, bh);
-                    if (!kFine) ah[1] = ah[3] = 0;
-                    mma16(c2, ah, bl);
+                    uint32_t bl[2];
+                    if (do_k || kFine) ldsm2(bl, right + kPlane + kk * 2);
+                    if (do_k) {
+                        uint32_t al[4];
+                        ldsm4(ah, at_lk + left + kk * 2);
+                        ldsm4(al, at_lk + kPlane + left + kk * 2);
+                        mma16(ck, ah, bh);
+                        mma16(ck1, al, bh);
+                        mma16(ck2, ah, bl);
+                    }
+                    if (do_q) {
+                        ldsm4(ah, at_lq + left + kk * 2);
+                        mma16(cq, ah, bh);
+                        if (kFine) mma16(cq, ah, bl);
+                    }
                 }
-                const int i = b * 16 + 8 + g, j = b * 16 + cc;
-                const float f = sm.beta[i] * down_kk;
+                // token rows and columns of the tile
+                const int i0 = wide ? 32 + m * 16 : m * 32 + 16;
+                const int j0 = wide ? nt * 8 : m * 32 + nt % 2 * 8;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    sm.l.L[i][j + e] = (c[e] + (c1[e] + c2[e])) * f;
-                    sm.A[i][j + e] = __float2half_rn((kFine ? c[2 + e] + c2[2 + e] : c[2 + e]) * kDownA);
+                for (int e = 0; e < 4; ++e) {
+                    const int i = i0 + g + e / 2 * 8, j = j0 + cc + e % 2;
+                    if (do_k) sm.l.L[i][j] = (ck[e] + (ck1[e] + ck2[e])) * (down_kk * sm.beta[i]);
+                    if (do_q) sm.A[i][j] = __float2half_rn(cq[e] * kDownA);
                 }
             }
-        } else {
-            const bool wide = half == 4;
-            const int m = b / 4;                              // 16-row tile of the left operand
-            const int nt = wide ? b % 4 : m * 2 + b / 2 % 2;  // 8-row tile of the right operand
-            const bool do_k = wide || b % 2 == 0, do_q = wide || b % 2 == 1;
-            float ck[4] = {}, ck1[4] = {}, ck2[4] = {}, cq[4] = {};
-            const uint32_t left = (uint32_t)((m * 16 + lane % 16) * kRow + lane / 16 * 8) * 2;
-            const uint32_t right = at_rk + (uint32_t)((nt * 8 + lane % 8) * kRow + (lane / 8 % 2) * 8) * 2;
+            __syncthreads();
+        }
+    } else {
+        // ---- one decay per token: k_i k_j and q_i k_j need no decayed operands, so k and q as
+        // they are (exact in one half) give both by one product, and the decays between i and
+        // j, products again, multiply the results.
 #pragma unroll
-            for (int kk = 0; kk < D; kk += 16) {
-                uint32_t ah[4], bh[2];
-                ldsm2(bh, right + kk * 2);
-                uint32_t bl[2];
-                if (do_k || kFine) ldsm2(bl, right + kPlane + kk * 2);
-                if (do_k) {
-                    uint32_t al[4];
-                    ldsm4(ah, at_lk + left + kk * 2);
-                    ldsm4(al, at_lk + kPlane + left + kk * 2);
-                    mma16(ck, ah, bh);
-                    mma16(ck1, al, bh);
-                    mma16(ck2, ah, bl);
-                }
-                if (do_q) {
-                    ldsm4(ah, at_lq + left + kk * 2);
-                    mma16(cq, ah, bh);
-                    if (kFine) mma16(cq, ah, bl);
-                }
+        for (int r = 0; r < 8; ++r) {
+            const int row = b * 8 + r;
+            *reinterpret_cast<Vec<__half2, P> *>(&sm.x.kq.k[row][lane * C]) = *reinterpret_cast<const Vec<__half2, P> *>(&k[r][0]);
+            *reinterpret_cast<Vec<__half2, P> *>(&sm.x.kq.q[row][lane * C]) = *reinterpret_cast<const Vec<__half2, P> *>(&q[r][0]);
+            if (lane == 0) sm.tmp[0][row / 16][row % 16] = a[r][0].x;
+        }
+        __syncthreads();
+        {
+            // sm.T[i][j] = the product of the decays after j up to i, zero above the diagonal:
+            // column j, 16 rows per thread
+            const int j = threadIdx.x % 64, part = threadIdx.x / 64;
+            float run = 1.0f;
+            for (int t = 0; t < part * 16; t += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(&sm.tmp[0][t / 16][t % 16]);
+                run *= (t > j ? x.x : 1.0f) * (t + 1 > j ? x.y : 1.0f);
+                run *= (t + 2 > j ? x.z : 1.0f) * (t + 3 > j ? x.w : 1.0f);
             }
-            // token rows and columns of the tile
-            const int i0 = wide ? 32 + m * 16 : m * 32 + 16;
-            const int j0 = wide ? nt * 8 : m * 32 + nt % 2 * 8;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = i0 + g + e / 2 * 8, j = j0 + cc + e % 2;
-                if (do_k) sm.l.L[i][j] = (ck[e] + (ck1[e] + ck2[e])) * (down_kk * sm.beta[i]);
-                if (do_q) sm.A[i][j] = __float2half_rn(cq[e] * kDownA);
+            for (int i = 0; i < 16; ++i) {
+                const int t = part * 16 + i;
+                run *= t > j ? sm.tmp[0][part][i] : 1.0f;
+                sm.T[t][j] = t >= j ? run : 0.0f;
             }
         }
         __syncthreads();
-    }
-    } else {
-    // ---- one decay per token: k_i k_j and q_i k_j need no decayed operands, so k and q as
-    // they are (exact in one half) give both by one product, and the decays between i and
-    // j, products again, multiply the results.
+        {
+            const uint32_t at_k = smem_u32(sm.x.kq.k), at_q = smem_u32(sm.x.kq.q);
+            for (int tile = b; tile < 20; tile += 8) {  // 16 x 8 tiles on and below the diagonal
+                const int m = (tile >= 2) + (tile >= 6) + (tile >= 12), nt = tile - m * (m + 1);
+                const uint32_t left = (uint32_t)((m * 16 + lane % 16) * kRow + lane / 16 * 8) * 2;
+                const uint32_t right = at_k + (uint32_t)((nt * 8 + lane % 8) * kRow + lane / 8 % 2 * 8) * 2;
+                float ck[4] = {}, cq[4] = {};
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        const int row = b * 8 + r;
-        *reinterpret_cast<Vec<__half2, P> *>(&sm.x.kq.k[row][lane * C]) = *reinterpret_cast<const Vec<__half2, P> *>(&k[r][0]);
-        *reinterpret_cast<Vec<__half2, P> *>(&sm.x.kq.q[row][lane * C]) = *reinterpret_cast<const Vec<__half2, P> *>(&q[r][0]);
-        if (lane == 0) sm.tmp[0][row / 16][row % 16] = a[r][0].x;
-    }
-    __syncthreads();
-    {
-        // sm.T[i][j] = the product of the decays after j up to i, zero above the diagonal:
-        // column j, 16 rows per thread
-        const int j = threadIdx.x % 64, part = threadIdx.x / 64;
-        float run = 1.0f;
-        for (int t = 0; t < part * 16; t += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(&sm.tmp[0][t / 16][t % 16]);
-            run *= (t > j ? x.x : 1.0f) * (t + 1 > j ? x.y : 1.0f);
-            run *= (t + 2 > j ? x.z : 1.0f) * (t + 3 > j ? x.w : 1.0f);
-        }
+                for (int kk = 0; kk < D; kk += 16) {
+                    uint32_t ak[4], aq[4], bk[2];
+                    ldsm2(bk, right + kk * 2);
+                    ldsm4(ak, at_k + left + kk * 2);
+                    ldsm4(aq, at_q + left + kk * 2);
+                    mma16(ck, ak, bk);
+                    mma16(cq, aq, bk);
+                }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = part * 16 + i;
-            run *= t > j ? sm.tmp[0][part][i] : 1.0f;
-            sm.T[t][j] = t >= j ? run : 0.0f;
-        }
-    }
-    __syncthreads();
-    {
-        const uint32_t at_k = smem_u32(sm.x.kq.k), at_q = smem_u32(sm.x.kq.q);
-        for (int tile = b; tile < 20; tile += 8) {  // 16 x 8 tiles on and below the diagonal
-            const int m = (tile >= 2) + (tile >= 6) + (tile >= 12), nt = tile - m * (m + 1);
-            const uint32_t left = (uint32_t)((m * 16 + lane % 16) * kRow + lane / 16 * 8) * 2;
-            const uint32_t right = at_k + (uint32_t)((nt * 8 + lane % 8) * kRow + lane / 8 % 2 * 8) * 2;
-            float ck[4] = {}, cq[4] = {};
-#pragma unroll
-            for (int kk = 0; kk < D; kk += 16) {
-                uint32_t ak[4], aq[4], bk[2];
-                ldsm2(bk, right + kk * 2);
-                ldsm4(ak, at_k + left + kk * 2);
-                ldsm4(aq, at_q + left + kk * 2);
-                mma16(ck, ak, bk);
-                mma16(cq, aq, bk);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = m * 16 + g + e / 2 * 8, j = nt * 8 + cc + e % 2;
-                const float decay = sm.T[i][j];
-                if (i > j) sm.l.L[i][j] = ck[e] * down_kk * decay * sm.beta[i];
-                sm.A[i][j] = __float2half_rn(cq[e] * kDownA * decay);
+                for (int e = 0; e < 4; ++e) {
+                    const int i = m * 16 + g + e / 2 * 8, j = nt * 8 + cc + e % 2;
+                    const float decay = sm.T[i][j];
+                    if (i > j) sm.l.L[i][j] = ck[e] * down_kk * decay * sm.beta[i];
+                    sm.A[i][j] = __float2half_rn(cq[e] * kDownA * decay);
+                }
             }
         }
-    }
-    __syncthreads();
-    // T's blocks above the diagonal are zeros again (their decays were), the others are written.
+        __syncthreads();
+        // T's blocks above the diagonal are zeros again (their decays were), the others are written.
     }
 
     // ---- T = (I + L)^-1, diagonal blocks of 16 by forward substitution, a column per lane
@@ -1434,60 +1434,60 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
         }
         if (warp == kCopyWarp && lane == 0) {
             // ---- the thread that takes items and copies operands
-        const int64_t step = (int64_t)p.heads * slot_bytes(D);
-        uint32_t n = 0, k = 0;
-        bool ok = true;
-        int *head = reinterpret_cast<int *>(w.ws), *counter = head + (kOut ? kHeadOut : kHeadSummary);
-        const int full = head[kHeadFull];
-        const int64_t items = (int64_t)(full + (kOut ? head[kHeadTail] : 0)) * p.heads;
-        int64_t next = blockIdx.x;
-        while (ok) {
-            const int64_t i = next;
-            Item it = {};
-            if (i < items) {
-                next = gridDim.x + (int64_t)atomicAdd(counter, 1);
-                it = load_item<D, kMode>(p, w, i, full);
-            }
-            if (k >= 2) ok = bar_wait(bar(kItemEmpty + (k & 1)), (k >> 1 & 1) ^ 1, abort);
-            if (!ok) break;
-            sm.item[k & 1] = it;
-            bar_arrive(bar(kItemFull + (k & 1)));
-            ++k;
-            if (it.chunks == 0) break;
-            if (it.from != nullptr)  // the next item's state, while the present one is walked
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(it.from), "r"(D * D * 4) : "memory");
-            for (int c = 0; c < it.chunks; ++c, ++n) {
-                const uint32_t par = n & 1, ring = n >> 1 & 1;
-                const uint32_t kst = Sm::kKStages == 2 ? par : 0, kring = Sm::kKStages == 2 ? ring : par;
-                const char *from = it.slots + c * step;
-                if (n >= 2) ok = bar_wait(bar(kWEmpty + par), ring ^ 1, abort);
-                if (!ok) break;
-                bar_expect(bar(kWFull + par), Sm::kWBytes);
-                if (kOut) {
-                    bulk_load(smem_u32(sm.w[par]), from + Slot<D>::qw, Sm::kWBytes, bar(kWFull + par));
-                } else {
-#pragma unroll
-                    for (int x = 0; x < D / 64; ++x)
-                        bulk_load(smem_u32(sm.w[par]) + x * 16384, from + Slot<D>::qw + x * Slot<D>::kBlock + 8192,
-                                  16384, bar(kWFull + par));
+            const int64_t step = (int64_t)p.heads * slot_bytes(D);
+            uint32_t n = 0, k = 0;
+            bool ok = true;
+            int *head = reinterpret_cast<int *>(w.ws), *counter = head + (kOut ? kHeadOut : kHeadSummary);
+            const int full = head[kHeadFull];
+            const int64_t items = (int64_t)(full + (kOut ? head[kHeadTail] : 0)) * p.heads;
+            int64_t next = blockIdx.x;
+            while (ok) {
+                const int64_t i = next;
+                Item it = {};
+                if (i < items) {
+                    next = gridDim.x + (int64_t)atomicAdd(counter, 1);
+                    it = load_item<D, kMode>(p, w, i, full);
                 }
-                if (n >= 2) ok = bar_wait(bar(kUEmpty + par), ring ^ 1, abort);
+                if (k >= 2) ok = bar_wait(bar(kItemEmpty + (k & 1)), (k >> 1 & 1) ^ 1, abort);
                 if (!ok) break;
-                bar_expect(bar(kUFull + par), kChunk * D * 4 + D * 4 + 64);
-                bulk_load(smem_u32(sm.u[par]), from + Slot<D>::u, kChunk * D * 4, bar(kUFull + par));
-                bulk_load(smem_u32(sm.meta[par]), from + Slot<D>::decay, D * 4 + 64, bar(kUFull + par));
-                if (Sm::kKStages == 2 ? n >= 2 : n >= 1) ok = bar_wait(bar(kKEmpty + kst), kring ^ 1, abort);
-                if (!ok) break;
-                bar_expect(bar(kKFull + kst), 2 * Slot<D>::kW);
-                bulk_load(smem_u32(sm.kk[kst]), from + Slot<D>::k_hi, 2 * Slot<D>::kW, bar(kKFull + kst));
-                if (kOut) {
-                    if (n >= 1) ok = bar_wait(bar(kAEmpty), par ^ 1, abort);
+                sm.item[k & 1] = it;
+                bar_arrive(bar(kItemFull + (k & 1)));
+                ++k;
+                if (it.chunks == 0) break;
+                if (it.from != nullptr)  // the next item's state, while the present one is walked
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(it.from), "r"(D * D * 4) : "memory");
+                for (int c = 0; c < it.chunks; ++c, ++n) {
+                    const uint32_t par = n & 1, ring = n >> 1 & 1;
+                    const uint32_t kst = Sm::kKStages == 2 ? par : 0, kring = Sm::kKStages == 2 ? ring : par;
+                    const char *from = it.slots + c * step;
+                    if (n >= 2) ok = bar_wait(bar(kWEmpty + par), ring ^ 1, abort);
                     if (!ok) break;
-                    bar_expect(bar(kAFull), kChunk * kChunk * 2);
-                    bulk_load(smem_u32(sm.a), from + Slot<D>::a, kChunk * kChunk * 2, bar(kAFull));
+                    bar_expect(bar(kWFull + par), Sm::kWBytes);
+                    if (kOut) {
+                        bulk_load(smem_u32(sm.w[par]), from + Slot<D>::qw, Sm::kWBytes, bar(kWFull + par));
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            bulk_load(smem_u32(sm.w[par]) + x * 16384, from + Slot<D>::qw + x * Slot<D>::kBlock + 8192,
+                                      16384, bar(kWFull + par));
+                    }
+                    if (n >= 2) ok = bar_wait(bar(kUEmpty + par), ring ^ 1, abort);
+                    if (!ok) break;
+                    bar_expect(bar(kUFull + par), kChunk * D * 4 + D * 4 + 64);
+                    bulk_load(smem_u32(sm.u[par]), from + Slot<D>::u, kChunk * D * 4, bar(kUFull + par));
+                    bulk_load(smem_u32(sm.meta[par]), from + Slot<D>::decay, D * 4 + 64, bar(kUFull + par));
+                    if (Sm::kKStages == 2 ? n >= 2 : n >= 1) ok = bar_wait(bar(kKEmpty + kst), kring ^ 1, abort);
+                    if (!ok) break;
+                    bar_expect(bar(kKFull + kst), 2 * Slot<D>::kW);
+                    bulk_load(smem_u32(sm.kk[kst]), from + Slot<D>::k_hi, 2 * Slot<D>::kW, bar(kKFull + kst));
+                    if (kOut) {
+                        if (n >= 1) ok = bar_wait(bar(kAEmpty), par ^ 1, abort);
+                        if (!ok) break;
+                        bar_expect(bar(kAFull), kChunk * kChunk * 2);
+                        bulk_load(smem_u32(sm.a), from + Slot<D>::a, kChunk * kChunk * 2, bar(kAFull));
+                    }
                 }
             }
-        }
         }
     }
     tc_before();
