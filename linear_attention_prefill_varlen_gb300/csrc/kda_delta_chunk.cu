@@ -206,9 +206,14 @@ __device__ __forceinline__ int64_t first_segment(const WalkArgs &w, int64_t star
     return (start + w.seg_tokens - 1) / w.seg_tokens + (start + w.seg_tokens) / (w.seg_tokens + 1);
 }
 
+constexpr int kTmpRow = 18;  // floats
+
 template <int D>
 struct PrepSmem {
     static constexpr int kRow = D + 8;  // halves: rows 16 bytes past a multiple of 128 bytes
+    // For D = 64 three blocks fit on an SM if v takes A's place once A is stored (it stays
+    // in registers until then, which the larger head has none left for).
+    static constexpr bool kVAfterA = D == 64;
     union {
         struct { __half lk_hi[32][kRow], lk_lo[32][kRow], lq[32][kRow], rk_hi[32][kRow], rk_lo[32][kRow]; } lv;
         struct { __half k_hi[64][kRow], k_lo[64][kRow]; } kg;
@@ -217,7 +222,7 @@ struct PrepSmem {
     } x;
     union {
         struct {
-            __half v[64][kRow];
+            __half v[kVAfterA ? 1 : 64][kVAfterA ? 8 : kRow];
             union {
                 float L[64][68];
                 struct { __half hi[64][72], lo[64][72]; } t;
@@ -227,13 +232,22 @@ struct PrepSmem {
     };
     float T[64][68];
     union {
-        float tmp[4][16][20];
+        alignas(16) float row_decay[64];  // decays, one per token
+        float tmp[4][16][kTmpRow];
         float down_t[64];  // unscaling of the rows of T diag(beta)
     };
-    __half A[64][72];
+    union {
+        alignas(16) __half A[64][72];
+        __half v_later[kVAfterA ? 64 : 1][kVAfterA ? kRow : 8];
+    };
     float block_decay[8][D];
     float beta[64];
     uint32_t top[3][8];  // per warp: largest |k| (then W), |q|, |v|
+
+    __device__ __forceinline__ __half (*v_rows())[kRow] {
+        if constexpr (kVAfterA) return v_later;
+        else return l.v;
+    }
 };
 
 __device__ __forceinline__ void prefetch_l2(const void *p) {
@@ -310,10 +324,14 @@ __device__ __forceinline__ float top_of(const uint32_t (&t)[8]) {
 
 __device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// Blocks of the preparation on an SM.
+template <int D>
+constexpr int kPrepBlocks = D == 64 ? 3 : 2;
+
 // One (chunk, head). Warp b holds tokens 8b .. 8b + 7 in registers, a lane C
 // channels of each.
 template <typename T, int D, bool kChannelGate, typename G>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(256, kPrepBlocks<D>)
     delta_prepare_kernel(const __grid_constant__ DeltaParams p, const __grid_constant__ WalkArgs w, int ahead) {
     constexpr int C = D / 32, P = C / 2;
     extern __shared__ __align__(1024) char raw_smem[];
@@ -363,7 +381,7 @@ __global__ void __launch_bounds__(256, 2)
     // ---- load; rows past the sequence's end are k = q = v = beta = 0, decay 1.
     // k and q stay as halves scaled by a power of two (exact but for values
     // below 2^-29 of the tile's largest), which halves their registers.
-    __half2 k[8][P], q[8][P];
+    __half2 k[8][P], q[8][P], v[PrepSmem<D>::kVAfterA ? 8 : 1][P];
     float2 a[8][P];
     float down_k, down_q, down_v;
     {
@@ -460,7 +478,12 @@ __global__ void __launch_bounds__(256, 2)
                 q[r][c] = __float22half2_rn(mul2(make_float2(to_f<T>(qv[r].v[2 * c]), to_f<T>(qv[r].v[2 * c + 1])), make_float2(up_q, up_q)));
                 f[c] = mul2(make_float2(to_f<T>(vv[r].v[2 * c]), to_f<T>(vv[r].v[2 * c + 1])), make_float2(up_v, up_v));
             }
-            store_row<P>(&sm.l.v[b * 8 + r][lane * C], f);
+            if constexpr (PrepSmem<D>::kVAfterA) {
+#pragma unroll
+                for (int c = 0; c < P; ++c) v[r][c] = __float22half2_rn(f[c]);
+            } else {
+                store_row<P>(&sm.v_rows()[b * 8 + r][lane * C], f);
+            }
         }
     }
     // A is kept as A up_q up_k 2^-22, below 2^15 since |A| < 2^(e_q + e_k + 9).
@@ -628,7 +651,7 @@ __global__ void __launch_bounds__(256, 2)
             const int row = b * 8 + r;
             *reinterpret_cast<Vec<__half2, P> *>(&sm.x.kq.k[row][lane * C]) = *reinterpret_cast<const Vec<__half2, P> *>(&k[r][0]);
             *reinterpret_cast<Vec<__half2, P> *>(&sm.x.kq.q[row][lane * C]) = *reinterpret_cast<const Vec<__half2, P> *>(&q[r][0]);
-            if (lane == 0) sm.tmp[0][row / 16][row % 16] = a[r][0].x;
+            if (lane == 0) sm.row_decay[row] = a[r][0].x;
         }
         __syncthreads();
         {
@@ -637,14 +660,14 @@ __global__ void __launch_bounds__(256, 2)
             const int j = threadIdx.x % 64, part = threadIdx.x / 64;
             float run = 1.0f;
             for (int t = 0; t < part * 16; t += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(&sm.tmp[0][t / 16][t % 16]);
+                const float4 x = *reinterpret_cast<const float4 *>(&sm.row_decay[t]);
                 run *= (t > j ? x.x : 1.0f) * (t + 1 > j ? x.y : 1.0f);
                 run *= (t + 2 > j ? x.z : 1.0f) * (t + 3 > j ? x.w : 1.0f);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int t = part * 16 + i;
-                run *= t > j ? sm.tmp[0][part][i] : 1.0f;
+                run *= t > j ? sm.row_decay[t] : 1.0f;
                 sm.T[t][j] = t >= j ? run : 0.0f;
             }
         }
@@ -760,6 +783,11 @@ __global__ void __launch_bounds__(256, 2)
     }
     __syncthreads();
 
+    if constexpr (PrepSmem<D>::kVAfterA)
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            *reinterpret_cast<Vec<__half2, P> *>(&sm.v_rows()[b * 8 + r][lane * C]) = *reinterpret_cast<const Vec<__half2, P> *>(&v[r][0]);
+
     // ---- T below its diagonal blocks: [X 0; Y Z]^-1 = [X^-1 0; -Z^-1 Y X^-1 Z^-1], for
     // pairs of 16 x 16 blocks, then of 32 x 32
     // A warp computes 8 columns (side) of a block.
@@ -769,9 +797,9 @@ __global__ void __launch_bounds__(256, 2)
             const int J = b / 2 * 32, I = J + 16;
             float c[3][4] = {}, d[3][4] = {};
             block_product(c, &sm.l.L[I][J], 68, &sm.T[J][J + side], 68, lane);
-            block_store(&sm.tmp[b / 2][0][side], 20, c, 1.0f, lane);
+            block_store(&sm.tmp[b / 2][0][side], kTmpRow, c, 1.0f, lane);
             __syncwarp();
-            block_product(d, &sm.T[I][I], 68, &sm.tmp[b / 2][0][side], 20, lane);
+            block_product(d, &sm.T[I][I], 68, &sm.tmp[b / 2][0][side], kTmpRow, lane);
             block_store(&sm.T[I][J + side], 68, d, -1.0f, lane);
         }
         __syncthreads();
@@ -779,10 +807,10 @@ __global__ void __launch_bounds__(256, 2)
         float c[3][4] = {}, d[3][4] = {};
         for (int m = J; m < 2; ++m)
             block_product(c, &sm.l.L[32 + I * 16][m * 16], 68, &sm.T[m * 16][J * 16 + side], 68, lane);
-        block_store(&sm.tmp[I * 2 + J][0][side], 20, c, 1.0f, lane);
+        block_store(&sm.tmp[I * 2 + J][0][side], kTmpRow, c, 1.0f, lane);
         __syncthreads();
         for (int m = 0; m <= I; ++m)
-            block_product(d, &sm.T[32 + I * 16][32 + m * 16], 68, &sm.tmp[m * 2 + J][0][side], 20, lane);
+            block_product(d, &sm.T[32 + I * 16][32 + m * 16], 68, &sm.tmp[m * 2 + J][0][side], kTmpRow, lane);
         block_store(&sm.T[32 + I * 16][J * 16 + side], 68, d, -1.0f, lane);
     }
     __syncthreads();
@@ -818,7 +846,7 @@ __global__ void __launch_bounds__(256, 2)
     __syncthreads();
     constexpr int NT = D / 64;  // 8-column tiles of a warp
     const uint32_t at_b = (uint32_t)(lane % 16 * kRow + b * NT * 8) * 2;
-    const uint32_t at_kg = smem_u32(sm.x.kg.k_hi) + at_b, at_v = smem_u32(sm.l.v) + at_b;
+    const uint32_t at_kg = smem_u32(sm.x.kg.k_hi) + at_b, at_v = smem_u32(sm.v_rows()) + at_b;
     const uint32_t at_t = smem_u32(sm.l.t.hi) + (uint32_t)(lane % 16 * 72 + lane / 16 * 8) * 2;
     float acc[4][NT][4] = {}, acu[4][NT][4] = {};
 #pragma unroll
@@ -1633,7 +1661,8 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
 
 // ------------------------------------------------------------------ host
 
-static_assert(2 * (sizeof(PrepSmem<128>) + 1024) <= 228 * 1024, "two blocks of the preparation per SM");
+static_assert(2 * (sizeof(PrepSmem<128>) + 1024) <= 228 * 1024 && 3 * (sizeof(PrepSmem<64>) + 1024) <= 228 * 1024,
+              "blocks of the preparation per SM");
 
 template <typename T, int D, bool kChannelGate, typename G>
 cudaError_t launch_prepare(const DeltaParams &p, const ChunkPlan &plan, const WalkArgs &w, kda_stream_t stream) {
@@ -1641,8 +1670,8 @@ cudaError_t launch_prepare(const DeltaParams &p, const ChunkPlan &plan, const Wa
     static std::atomic<uint64_t> done;
     const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), (int)sizeof(PrepSmem<D>), done);
     if (e != cudaSuccess) return e;
-    // Two blocks per SM run at a time, a token chunk's heads next to each other.
-    const int ahead = (int)(2 * current_sms() / p.heads) * kChunk;
+    // A token chunk's heads are next to each other in the grid.
+    const int ahead = (int)(kPrepBlocks<D> * current_sms() / p.heads) * kChunk;
     return launch(kernel, dim3((unsigned)(plan.slots * p.heads)), 256, sizeof(PrepSmem<D>), stream, p, w, ahead);
 }
 
