@@ -1,5 +1,6 @@
 // The gated delta rule on the state's rows in registers (include/kda_layer.h,
-// kda_delta_t): one token per sequence, and whole sequences.
+// kda_delta_t): one token per sequence (the update kernel, below), short sequences
+// and FP32's (the rows kernel, with its own comment), and the C entries.
 //
 // The rows v of a state are independent: row v needs only v_t[v], and k, q, beta
 // and the decays that all rows share. A warp keeps rows of one head's state in
@@ -9,7 +10,7 @@
 // so that both dot products run on S' together and o needs no second pass.
 //
 // Bound: for one token the state, read and written once, in HBM (1024 tokens of
-// 12 heads: 250 us, 6.49 TB/s, 97% of a device copy's rate).
+// 12 heads: 245.6 us, 6.62 TB/s, 99% of a device copy's rate).
 #include <type_traits>
 
 #include "kda_delta_chunk.cuh"
@@ -159,8 +160,13 @@ __global__ void __launch_bounds__(kWarps * 32) delta_update_kernel(const __grid_
 // registers, into slots of shared memory in fragment order (a 16-byte piece per
 // lane and 8-column tile, at piece ^ (tile % 8) against bank conflicts).
 //
-// Bound: the tensor core's tf32 rate (512 multiply-adds per clock and SM): 118
-// products per warp and group are 236 clocks per token and head of 128.
+// Bound: latency. The state's 64 registers per thread leave an SM 12 warps (of 168
+// registers), three per scheduler, which cover neither the products' chains nor the
+// fetches of the two roles' straight-line code: 256 sequences of 32 tokens, 12 heads
+// of 128, bf16: 304 us, 3.7 us per group on an SM, tf32 pipe 25%, issue slots 30%,
+// HBM 20%. 6 and 8 preparing warps (128 registers, spills) took 462 and 456 us a call
+// against 341; the tokens one at a time in FP32 were slower by a quarter (682 us
+// against 548 at 256 sequences of 64).
 constexpr int kGroup = 8;
 
 template <typename T, int D>
@@ -617,7 +623,8 @@ DeltaParams params_of(const kda_delta_t *d) {
 // path's launches 35 us; on a full GPU a group costs a seventh of a chunk (bf16, 12
 // heads of 128, us, groups against chunks: one sequence of 96 tokens 24 against 38,
 // of 192 43 against 41; 256 sequences of 32 297 against 495, of 64 548 against 500;
-// 256 sequences of 1 to 128 among 1024 of one 893 with 32 here, 965 with 72).
+// 256 sequences of 1 to 128 among 1024 of one 982, 972 and 1006 with 16, 32 and 48
+// here; one of 8192 among 99 of 1 to 80 495, 523 and 499).
 int short_len(int64_t num_seqs, int64_t heads, int sms) {
     return num_seqs * heads * 2 <= (int64_t)sms ? 112 : 32;
 }

@@ -26,8 +26,8 @@
 // Precision: the state path is FP32. Tensor-core operands on it are pairs of
 // halves, x 2^s = hi + lo with 22 bits, s taken from the largest value of the
 // tile (of the row for S and V'), and three products hi hi, hi lo, lo hi summed
-// in FP32. What feeds only o (q G, A, and S and V' there) is one half: 11 bits
-// against the 8 or 11 of the output's type.
+// in FP32. What feeds only o (q G, A, and S and V' there) is one half for bf16 x: 11
+// bits against the output's 8; for fp16 x S, V' and k there keep their second halves.
 #include "kda_delta_chunk.cuh"
 
 #include <type_traits>
@@ -324,12 +324,18 @@ __device__ __forceinline__ float top_of(const uint32_t (&t)[8]) {
 
 __device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// Blocks of the preparation on an SM.
+// Blocks of the preparation on an SM. With 3 instead of 2 for heads of 64: 303 us against
+// 348 (4 x 8192 tokens, 17 heads, fp16).
 template <int D>
 constexpr int kPrepBlocks = D == 64 ? 3 : 2;
 
 // One (chunk, head). Warp b holds tokens 8b .. 8b + 7 in registers, a lane C
 // channels of each.
+//
+// Bound: latency and issue. 16384 tokens, 12 heads of 128, bf16: 248 us; HBM 28% (230 MB
+// read, 319 written), issue slots 44%, mma.sync 13%; two blocks of 8 warps per SM, by
+// registers (128) and shared memory (115 KB), between whose phases barriers, shared-memory
+// latency and loads share the stalls about evenly.
 template <typename T, int D, bool kChannelGate, typename G>
 __global__ void __launch_bounds__(256, kPrepBlocks<D>)
     delta_prepare_kernel(const __grid_constant__ DeltaParams p, const __grid_constant__ WalkArgs w, int ahead) {
@@ -1091,10 +1097,6 @@ __device__ __forceinline__ Item load_item(const DeltaParams &p, const WalkArgs &
     return it;
 }
 
-// Blocks stay resident and take the next item from a counter in the workspace
-// (which block gets an item changes nothing in its result); the copy warp runs
-// ahead into the next item. Every role keeps a running chunk number n for
-// the rings' parities.
 // Two results rounded to T, the first in the lower half.
 template <typename T>
 __device__ __forceinline__ uint32_t round2(float2 f) {
@@ -1103,6 +1105,15 @@ __device__ __forceinline__ uint32_t round2(float2 f) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// Bound: the chain through a chunk (P, V' = U - P, the state's update and its rounding
+// to halves), with the operands of the next chunk already in shared memory. 16384 tokens,
+// 12 heads of 128, bf16: summaries 93 us (tcgen05 38% of active clocks; 139 with one walk
+// at a time per block), outputs 79 to 81 us (28%; 389 MB read, HBM 67%).
+//
+// Blocks stay resident and take the next item from a counter in the workspace
+// (which block gets an item changes nothing in its result); the copy warp runs
+// ahead into the next item. Every role keeps a running chunk number n for
+// the rings' parities.
 template <typename T, int D, int kMode>
 __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
     delta_walk_kernel(const __grid_constant__ DeltaParams p, const __grid_constant__ WalkArgs w) {
@@ -1537,6 +1548,9 @@ __global__ void __launch_bounds__(kWalkThreads<kMode>, 1)
 
 // ------------------------------------------------------------------ join
 
+// (31 us for 16384 tokens, 12 heads of 128: 12 segments in turn, each a 16 x 128 x 128 FP32
+// product per block, M's 64 KB from L2.)
+//
 // For each sequence of several segments: start[0] = the cached state (the walk
 // of the last segment overwrites it), start[seg + 1] = (seg ? start[seg] M[seg]
 // : 0) + B[seg], segment by segment. A block takes kJoinRows rows of one

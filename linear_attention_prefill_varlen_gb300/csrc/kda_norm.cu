@@ -67,7 +67,7 @@ struct GatedParams {
 // in registers, so x is read once and the sum of squares is a butterfly. A block
 // takes kBatch times as many heads as it has groups of lanes, a block's width
 // apart, with all their loads issued first: one head's two loads per thread leave
-// too few bytes in flight.
+// too few bytes in flight (16384 x 12 x 128 bf16: 27.5 us, 5.50 TB/s; 34.8 with one).
 template <typename T, int kLanes, int kVpl, int kBatch, int kAct>
 __global__ void __launch_bounds__(256) gated_rmsnorm_kernel(const __grid_constant__ GatedParams p) {
     constexpr int N = 16 / sizeof(T), kPerBlock = 256 / kLanes;
@@ -198,7 +198,8 @@ constexpr int kRowsAhead = kVpt < 4 ? 2 : 1;  // the widest rows' pieces fill 12
 // row, keeps y and then r in registers between the reductions, and has its pieces
 // of the next kRowsAhead rows on their way into its own part of shared memory (it
 // alone reads them, so no barrier guards them): held in registers they would leave
-// too few threads on the SM to keep HBM busy.
+// too few threads on the SM to keep HBM busy (16384 x 4608 bf16: 118.6 us, 6.37 TB/s,
+// 95% of a copy's rate; 160 one row at a time, 277 with the next row in registers).
 template <typename T, typename R, int kVpt, int kAct, bool kPost>
 __global__ void __launch_bounds__(512) residual_rmsnorm_kernel(const __grid_constant__ ResidualParams p) {
     constexpr bool kGate = kAct != KDA_NORM_GATE_NONE;
